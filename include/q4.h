@@ -373,6 +373,139 @@ Q4_API q4_status q4_gptq_prepare(const double *H, int64_t K, double damp, double
 Q4_API q4_status q4_gptq_quantize(const float *w, int64_t N, int64_t K, const double *U, int bits,
                 int64_t group, uint8_t *payload, float *scales, int threads);
 
+/*
+ * ---- 8-bit floating point with a scale per block of 128, and routed experts.
+ * The codes are e4m3 (1 sign, 4 exponent, 3 mantissa bits; largest finite value 448), one
+ * byte each, with one fp32 scale per block: 128 consecutive values of a row of activations,
+ * or 128 rows x 128 columns of a weight matrix. Blocks at an edge hold what is left.
+ */
+typedef enum q4_dtype {
+    Q4_F32 = 0,  /* float32 */
+    Q4_BF16 = 1, /* bfloat16 */
+    Q4_F16 = 2   /* float16 */
+} q4_dtype;
+
+/* q4_fp8_pack flags. */
+#define Q4_FP8_PACK_SILU_MUL 1u
+
+/*
+ * q4_fp8_pack -- quantize rows of activations: per block of 128 values of a row,
+ *   scale = max|v| / 448 in fp32 (one IEEE division), 0 -> 1;
+ *   code  = e4m3(v / scale): one IEEE fp32 division, rounded to nearest, ties to even,
+ *           magnitudes above 448 held at 448.
+ *   x        [x_rows][K] of type xt, row-major, any alignment (16-byte aligned rows are
+ *            read fastest); with Q4_FP8_PACK_SILU_MUL [x_rows][2K], gate then up, and the
+ *            values are v = silu(gate) * up = gate * up / (1 + exp(-gate)) in fp32
+ *   rows     optional (may be NULL) [R] int32: output row i takes row rows[i] of x (the
+ *            tokens of q4_moe_sort); an entry outside 0 .. x_rows - 1 leaves output row i as
+ *            it was. Without it R must be x_rows.
+ *   count    optional (may be NULL) device int32: output rows from *count on are left as
+ *            they were (offsets + E of q4_moe_sort: the rows that have an expert)
+ *   codes    out, [R][K] bytes
+ *   scales   out, [R][ceil(K / 128)] fp32
+ *   status_word  optional, as qpack's: Q4_STATUS_NONFINITE where a block holds Inf or NaN
+ *            (its outputs are then unspecified)
+ * Errors: Q4_ERR_ARG (null pointers, types, flags, sizes), Q4_ERR_UNSUPPORTED (K > 2^30, more
+ * than 2^31 - 1 blocks), Q4_ERR_CUDA. R == 0 or x_rows == 0 enqueues nothing.
+ */
+Q4_API q4_status q4_fp8_pack(const void *x, q4_dtype xt, int64_t x_rows, int64_t K, const int32_t *rows, int64_t R,
+                const int32_t *count, uint32_t flags, uint8_t *codes, float *scales, uint32_t *status_word,
+                void *stream);
+
+/*
+ * q4_fp8_pack_weights -- quantize E weight matrices by the same rule, a block being 128 rows
+ * x 128 columns of one matrix.
+ *   w        [E][N][K] of type wt (E = 1: one matrix)
+ *   codes    out, [E][N][K] bytes
+ *   scales   out, [E][ceil(N / 128)][ceil(K / 128)] fp32
+ *   status_word  as q4_fp8_pack's
+ * Errors: as q4_fp8_pack. E * N == 0 enqueues nothing.
+ */
+Q4_API q4_status q4_fp8_pack_weights(const void *w, q4_dtype wt, int64_t E, int64_t N, int64_t K, uint8_t *codes,
+                float *scales, uint32_t *status_word, void *stream);
+
+/*
+ * q4_fp8_gemm -- y[m][n] = sum over blocks b of K:
+ *     xs[m][b] * ws[n / 128][b] * sum over k in b of x[m][k] * w[n][k].
+ *   x, xs    [M][K] codes and [M][ceil(K / 128)] scales (q4_fp8_pack); x 16-byte aligned
+ *   w, ws    [N][K] codes and [ceil(N / 128)][ceil(K / 128)] scales (q4_fp8_pack_weights, or a
+ *            checkpoint of that layout); w 16-byte aligned
+ *   y        out, [M][N] of type yt, rounded once from the fp32 sums
+ *   status_word  as qgemm's: Q4_STATUS_TIMEOUT where a bounded wait gave up
+ * K must be a multiple of 16 (else Q4_ERR_UNSUPPORTED), M and N are any. No workspace. The
+ * inner sums are exact products added in fp32 on the tensor cores; the order of all sums
+ * depends on the sizes only, so results are the same on every run. A row of x that holds NaN
+ * codes affects its own row of y alone.
+ * Errors: Q4_ERR_ARG (null pointers, types, sizes), Q4_ERR_UNSUPPORTED (K % 16, M, N or K >
+ * 2^30, misaligned codes), Q4_ERR_CUDA. M == 0 or N == 0 enqueues nothing.
+ */
+Q4_API q4_status q4_fp8_gemm(const uint8_t *x, const float *xs, int64_t M, const uint8_t *w, const float *ws, int64_t N,
+                int64_t K, void *y, q4_dtype yt, uint32_t *status_word, void *stream);
+
+/*
+ * q4_fp8_gemm_grouped -- the same product for rows sorted by expert.
+ *   x, xs    [R][K] codes and their scales
+ *   offsets  [E + 1] device int32, not descending: rows offsets[e] .. offsets[e + 1] - 1 are
+ *            expert e's (q4_moe_sort). An expert may have no rows. Rows that no expert has
+ *            (before offsets[0], from offsets[E] on) are left as they were in y.
+ *   w, ws    [E][N][K] codes and [E][ceil(N / 128)][ceil(K / 128)] scales
+ *   Other arguments as q4_fp8_gemm.
+ * Offsets outside 0 .. R or descending give unspecified rows of y, never an access outside
+ * the arrays.
+ * Errors: as q4_fp8_gemm, and Q4_ERR_UNSUPPORTED for E > 1024 or E * N > 2^31 - 1.
+ */
+Q4_API q4_status q4_fp8_gemm_grouped(const uint8_t *x, const float *xs, int64_t R, const int32_t *offsets, int64_t E,
+                const uint8_t *w, const float *ws, int64_t N, int64_t K, void *y, q4_dtype yt, uint32_t *status_word,
+                void *stream);
+
+/*
+ * q4_moe_sort -- sort the choices of T tokens by expert (stable: within an expert by token,
+ * then by choice).
+ *   ids      [T][k] expert of each choice, int32 or int64 (ids_bits = 32 or 64). An id outside
+ *            0 .. E - 1 drops the choice (a padded token).
+ *   tokens   out, [T * k] int32: the token at each sorted place; -1 from offsets[E] on
+ *   pos      out, [T][k] int32: the sorted place of each choice; -1 where it was dropped
+ *   offsets  out, [E + 1] int32: expert e has the places offsets[e] .. offsets[e + 1] - 1
+ * Errors: Q4_ERR_ARG (null pointers, ids_bits, sizes, k < 1, E < 1), Q4_ERR_UNSUPPORTED
+ * (E > 1024, T * k > 2^31 - 1), Q4_ERR_CUDA. T == 0 still writes offsets (zeros).
+ */
+Q4_API q4_status q4_moe_sort(const void *ids, int ids_bits, int64_t T, int64_t k, int64_t E, int32_t *tokens,
+                int32_t *pos, int32_t *offsets, void *stream);
+
+/*
+ * q4_moe_gather -- xs[i] = x[tokens[i]] for i < R, rows of D values of type xt. An entry outside
+ * 0 .. T - 1 (the -1 of q4_moe_sort) leaves row i as it was. Its gradient is q4_moe_combine
+ * without weights.
+ * Errors: Q4_ERR_ARG, Q4_ERR_UNSUPPORTED (D > 2^30, R or the row chunks > 2^31 - 1), Q4_ERR_CUDA.
+ */
+Q4_API q4_status q4_moe_gather(const void *x, q4_dtype xt, int64_t T, int64_t D, const int32_t *tokens, int64_t R,
+                void *xs, void *stream);
+
+/*
+ * q4_moe_combine -- out[t] = sum over j of weights[t][j] * ys[pos[t][j]], in fp32 with j
+ * ascending, rounded once.
+ *   ys       [R][D] of type yt
+ *   pos      [T][k] int32 (q4_moe_sort); an entry outside 0 .. R - 1 adds nothing
+ *   weights  [T][k] fp32, or NULL for all ones
+ *   out      out, [T][D] of type yt; must not overlap ys
+ * Errors: as q4_moe_gather.
+ */
+Q4_API q4_status q4_moe_combine(const void *ys, q4_dtype yt, int64_t R, int64_t D, const int32_t *pos,
+                const float *weights, int64_t T, int64_t k, void *out, void *stream);
+
+/*
+ * q4_moe_combine_backward -- the gradients of q4_moe_combine for dout [T][D]:
+ *   dys[pos[t][j]] = weights[t][j] * dout[t]      [R][D] of type yt; rows that no pos names
+ *                                                 are left as they were
+ *   dweights[t][j] = sum over d of dout[t][d] * ys[pos[t][j]][d]   [T][k] fp32; 0 where pos is
+ *                                                 outside 0 .. R - 1
+ * The entries of pos inside 0 .. R - 1 must differ from one another (q4_moe_sort's do).
+ * Errors: as q4_moe_gather.
+ */
+Q4_API q4_status q4_moe_combine_backward(const void *dout, const void *ys, q4_dtype yt, int64_t R, int64_t D,
+                const int32_t *pos, const float *weights, int64_t T, int64_t k, void *dys, float *dweights,
+                void *stream);
+
 #ifdef __cplusplus
 }
 #endif

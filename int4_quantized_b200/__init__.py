@@ -26,6 +26,8 @@ __all__ = [
     "Q4Error", "lib", "lib_path", "payload_bytes", "num_scales", "qgemm_workspace_bytes",
     "qpack", "qdequant", "qgemm", "qgemm_noalloc", "StackGemv", "DecodeStack", "gptq_hessian", "gptq_prepare", "gptq_quantize", "gptq_pack", "NOALLOC_SCRATCH_BYTES", "Q4_OK", "Q4_ERR_ARG", "Q4_ERR_UNSUPPORTED", "Q4_ERR_CUDA",
     "Q4_ERR_NONFINITE", "Q4_ERR_WORKSPACE", "Q4_ERR_SCRATCH_LIMIT", "Q4_X_F32", "Q4_X_BF16", "Q4_QGEMM_WEIGHTS_STATIC", "STATUS_NONFINITE", "STATUS_TIMEOUT",
+    "fp8_pack", "fp8_pack_weights", "fp8_gemm", "fp8_gemm_grouped", "moe_sort", "moe_gather", "moe_combine",
+    "moe_combine_backward", "Fp8Experts",
 ]
 
 Q4_OK, Q4_ERR_ARG, Q4_ERR_UNSUPPORTED, Q4_ERR_CUDA, Q4_ERR_NONFINITE, Q4_ERR_WORKSPACE, \
@@ -97,6 +99,22 @@ def lib() -> ctypes.CDLL:
                 L.q4_gptq_prepare.restype = i32
                 L.q4_gptq_quantize.argtypes = [vp, i64, i64, vp, i32, i64, vp, vp, i32]
                 L.q4_gptq_quantize.restype = i32
+                L.q4_fp8_pack.argtypes = [vp, i32, i64, i64, vp, i64, vp, ctypes.c_uint32, vp, vp, vp, vp]
+                L.q4_fp8_pack.restype = i32
+                L.q4_fp8_pack_weights.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp]
+                L.q4_fp8_pack_weights.restype = i32
+                L.q4_fp8_gemm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, vp, vp]
+                L.q4_fp8_gemm.restype = i32
+                L.q4_fp8_gemm_grouped.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i32, vp, vp]
+                L.q4_fp8_gemm_grouped.restype = i32
+                L.q4_moe_sort.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp]
+                L.q4_moe_sort.restype = i32
+                L.q4_moe_gather.argtypes = [vp, i32, i64, i64, vp, i64, vp, vp]
+                L.q4_moe_gather.restype = i32
+                L.q4_moe_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp]
+                L.q4_moe_combine.restype = i32
+                L.q4_moe_combine_backward.argtypes = [vp, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, vp]
+                L.q4_moe_combine_backward.restype = i32
                 _lib = L
     return _lib
 
@@ -376,3 +394,8 @@ def gptq_pack(w, x, bits: int, group: int, damp: float = 0.01, threads: int = 0)
     """GPTQ end to end on the host: H from calibration inputs x [rows, K], then the codes."""
     H = gptq_hessian(x, threads=threads)
     return gptq_quantize(w, gptq_prepare(H, damp, threads), bits, group, threads)
+
+
+# ---- 8-bit floating point and routed experts (their modules use the helpers above) ---------
+from .fp8 import fp8_gemm, fp8_gemm_grouped, fp8_pack, fp8_pack_weights  # noqa: E402
+from .moe import Fp8Experts, moe_combine, moe_combine_backward, moe_gather, moe_sort  # noqa: E402

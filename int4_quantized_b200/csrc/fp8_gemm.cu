@@ -1,0 +1,462 @@
+// fp8_gemm.cu -- the product of e4m3 codes with a scale per block of 128, dense and by experts.
+//
+// y[m][n] = sum over blocks b of 128 k: xs[m][b] * ws[n / 128][b] * sum over k in b of x[m][k] w[n][k]
+// (with experts: rows offsets[e] .. offsets[e + 1] - 1 of x take the weights and scales of
+// expert e). The inner sums run on the tensor cores (tcgen05 kind::f8f6f4, exact products,
+// fp32 sums in tensor memory); each block's sum is then multiplied by its two scales and
+// added in fp32 registers ("promotion"), and y is rounded once.
+//
+// Few rows (fp8_stream): A = 128 weight rows, B = 16 to 128 rows of x, so that the weights,
+// which are nearly all the bytes, fill the tensor core's long side; D = 128 lanes (weight
+// rows) x NT columns (rows of x). K is split over a thread-block cluster where the tiles
+// alone would leave SMs without work; the CTAs then exchange their partial sums through
+// distributed shared memory and add them in a fixed order.
+//   warp 0      TMA producer: 128 x 128 weights and NT x 128 codes of x a block of k
+//   warp 1      tensor memory, MMA issue (4 instructions of 32 k a block)
+//   warp 2      the rows' scales of each block, by 4-byte asynchronous copies
+//   warps 4-7   promotion and stores; lane = weight row, so stores of y are contiguous
+// Every wait is bounded (about one second); one that gives up sets Q4_STATUS_TIMEOUT in the
+// status word, and the roles run to completion without further waits.
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace q4 {
+
+namespace {
+
+constexpr int kBK = 128;             // k per block: one 128-byte swizzle row of codes
+constexpr int kWRows = 128;          // weight rows per tile
+constexpr int kWBytes = kWRows * kBK;
+constexpr int kMaxExperts = 1024;
+
+struct Fp8Args {
+    const float *xs;         // [R][kb]
+    const float *ws;         // [E][nb][kb]
+    const int32_t *offsets;  // [E + 1] on the device, or null: one expert, rows 0 .. R - 1
+    void *y;
+    uint32_t *status;
+    int64_t N;
+    int32_t R, E;
+    int32_t nb, kb;          // blocks of 128 along N and K
+    int32_t split;           // CTAs of a cluster that share one tile's K
+    int32_t stages;          // ring depth
+};
+
+// The experts' rows and tiles, worked out once a block: expert e has the rows rows0[e] ..
+// rows0[e + 1] - 1 and first[e] row tiles come before its own (first[E] in all). Offsets are
+// taken as a running maximum held inside 0 .. R, so that whatever stands there, the experts'
+// rows follow one another inside x and y. Called by the whole block; ends without a barrier.
+Q4_DEVINL void count_tiles(const Fp8Args &a, int tile_rows, int32_t *first, int32_t *rows0) {
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x;
+    int32_t carry = 0, high = 0;
+    for (int b = 0; b <= a.E; b += 32) {
+        const int e = b + lane;
+        int32_t m = a.offsets ? (e <= a.E ? a.offsets[e] : 0) : (e == 0 ? 0 : a.R);
+        m = max(high, min(m, a.R));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, v);
+        }
+        // expert e - 1 ends where expert e begins
+        const int32_t before = __shfl_up_sync(0xffffffffu, m, 1);
+        const int32_t n = (m - (lane ? before : high) + tile_rows - 1) / tile_rows;
+        int32_t x = n;  // lane 0 of the first chunk has no expert before it: rows 0 .. offsets[0] - 1 are nobody's
+        if (e == 0) x = 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += v;
+        }
+        if (e <= a.E) {
+            rows0[e] = m;
+            first[e] = carry + x;
+        }
+        carry += __shfl_sync(0xffffffffu, x, 31);
+        high = __shfl_sync(0xffffffffu, m, 31);
+    }
+}
+
+struct Tile {
+    int e, nb;       // expert, weight block
+    int row0, rows;  // rows of x
+};
+// Tile j of first[E] * nb: by expert, then weight block, then row tile, so that the row tiles
+// that share weights come one after the other and find them in L2.
+Q4_DEVINL Tile tile_at(const Fp8Args &a, int tile_rows, const int32_t *first, const int32_t *rows0, int64_t j) {
+    // the expert: the last e with first[e] * nb <= j
+    int lo = 0, hi = a.E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)first[mid] * a.nb <= j) lo = mid;
+        else hi = mid;
+    }
+    // several experts without rows share a first tile: the last of them is the one with rows
+    const int n = first[lo + 1] - first[lo];
+    const int64_t i = j - (int64_t)first[lo] * a.nb;
+    Tile t;
+    t.e = lo;
+    t.nb = (int)(i / n);
+    t.row0 = rows0[lo] + (int)(i - (int64_t)t.nb * n) * tile_rows;
+    t.rows = min(tile_rows, rows0[lo + 1] - t.row0);
+    return t;
+}
+
+template <typename Y>
+Q4_DEVINL Y round_to(float v) {
+    if constexpr (std::is_same<Y, float>::value) return v;
+    else if constexpr (std::is_same<Y, __half>::value) return __float2half_rn(v);
+    else return __float2bfloat16_rn(v);
+}
+
+Q4_DEVINL uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+Q4_DEVINL uint32_t map_rank(uint32_t smem_addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
+    return r;
+}
+Q4_DEVINL void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+Q4_DEVINL void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+Q4_DEVINL void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+Q4_DEVINL void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- few rows ---------------------------------------------------------------------------
+constexpr int kStreamThreads = 256;
+template <int NT>
+struct Stream {
+    static constexpr int kXBytes = NT * kBK;
+    static constexpr int kStage = kWBytes + kXBytes;
+    static constexpr int kBufs = NT <= 32 ? 8 : 256 / NT;  // tensor-memory buffers of NT columns
+    static constexpr int kCols = kBufs * NT;               // 128 or 256 of the 512 columns
+    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kWRows >> 4) << 24);
+    // ring, exchange buffer of the split sums, scales, barriers
+    static size_t smem(int stages, int split, int E) {
+        return 1024 + (size_t)stages * kStage + (split > 1 ? (size_t)kWRows * NT * 4 : 0) + kBufs * NT * 4 +
+               (2 * (size_t)stages + 3 * kBufs + 2) * 8 + 16 + (size_t)(2 * E + 2) * 4;
+    }
+};
+
+template <int NT, typename Y>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw) {
+    using S = Stream<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *p = ring + (size_t)a.stages * S::kStage;
+    float *parts = reinterpret_cast<float *>(p);  // [split][NT / split][128]
+    if (a.split > 1) p += kWRows * NT * 4;
+    float *xsc = reinterpret_cast<float *>(p);  // [kBufs][NT]
+    uint64_t *full = reinterpret_cast<uint64_t *>(p + S::kBufs * NT * 4);
+    uint64_t *empty = full + a.stages;
+    uint64_t *dfull = empty + a.stages;
+    uint64_t *dempty = dfull + S::kBufs;
+    uint64_t *sfull = dempty + S::kBufs;
+    uint64_t *done = sfull + S::kBufs;
+    uint64_t *joined = done + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(joined + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 4);
+    int32_t *rows0 = first + a.E + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < S::kBufs; ++i) {
+            mbar_init(dfull + i, 1);
+            mbar_init(dempty + i, 4);
+            mbar_init(sfull + i, 32);
+        }
+        mbar_init(done, 1);
+        mbar_init(joined, 4 * a.split);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(tmem_slot, S::kCols);
+        tmem_relinquish();
+    }
+    count_tiles(a, NT, first, rows0);
+    tc_fence_before();
+    __syncthreads();
+    if (a.split > 1) cluster_sync_all();  // every CTA's barriers stand before another arrives on them
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+    const int64_t tiles = (int64_t)first[a.E] * a.nb;
+    // a split tile is its cluster's only one: the exchange buffer is used once
+    const int64_t step = a.split > 1 ? tiles : gridDim.x, tile0 = blockIdx.x / a.split;
+    const int k0 = (int)((int64_t)a.kb * rank / a.split), k1 = (int)((int64_t)a.kb * (rank + 1) / a.split);
+    bool timed_out = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+                const Tile t = tile_at(a, NT, first, rows0, j);
+                const int wrow = (int)(t.e * a.N + (int64_t)t.nb * kWRows);
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = it % a.stages;
+                    if (it >= a.stages) timed_out = !mbar_wait(empty + s, (uint32_t)((it / a.stages - 1) & 1));
+                    if (timed_out) break;
+                    uint8_t *st = ring + (size_t)s * S::kStage;
+                    mbar_arrive_expect_tx(full + s, S::kStage);
+                    tma_load_2d(st, &tmw, full + s, kb * kBK, wrow);
+                    tma_load_2d(st + kWBytes, &tmx, full + s, kb * kBK, t.row0);
+                }
+            }
+            // no copy may land after the block has gone
+            for (int i = max(0, it - a.stages); i < it; ++i)
+                timed_out |= !mbar_wait(full + i % a.stages, (uint32_t)((i / a.stages) & 1));
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = it % a.stages, d = it % S::kBufs;
+                    if (it >= S::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / S::kBufs - 1) & 1));
+                    if (!timed_out) timed_out = !mbar_wait(full + s, (uint32_t)((it / a.stages) & 1));
+                    if (timed_out) break;
+                    tc_fence_after();
+                    const uint8_t *st = ring + (size_t)s * S::kStage;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 32; ++kk)
+                        umma_f8(tmem + (uint32_t)(d * NT), sw128_desc(st + kk * 32), sw128_desc(st + kWBytes + kk * 32),
+                                S::kIdesc, kk > 0 ? 1u : 0u);
+                    umma_commit(empty + s);
+                    umma_commit(dfull + d);
+                }
+            }
+            umma_commit(done);
+            timed_out |= !mbar_wait(done, 0);
+        }
+    } else if (warp == 2) {
+        int it = 0;
+        for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+            const Tile t = tile_at(a, NT, first, rows0, j);
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                const int d = it % S::kBufs;
+                if (it >= S::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / S::kBufs - 1) & 1));
+                if (timed_out) break;
+#pragma unroll
+                for (int c = 0; c < NT; c += 32) {
+                    const int col = c + lane;
+                    if (col < NT)
+                        cp_async4(xsc + d * NT + col,
+                                  a.xs + (int64_t)(t.row0 + min(col, t.rows - 1)) * a.kb + kb);
+                }
+                cp_async_arrive(sfull + d);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= 4) {
+        const int q = warp & 3, rl = 32 * q + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+        Y *const y = static_cast<Y *>(a.y);
+        int it = 0;
+        for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+            const Tile t = tile_at(a, NT, first, rows0, j);
+            const float *wsc = a.ws + ((int64_t)t.e * a.nb + t.nb) * a.kb;
+            const int64_t n = (int64_t)t.nb * kWRows + rl;
+            uint64_t acc[NT / 2];
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) acc[i] = 0ull;
+            float w_next = k0 < k1 ? wsc[k0] : 0.f;
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                const int d = it % S::kBufs;
+                const float wv = w_next;
+                if (kb + 1 < k1) w_next = wsc[kb + 1];
+                timed_out = !mbar_wait(sfull + d, (uint32_t)((it / S::kBufs) & 1));
+                if (!timed_out) timed_out = !mbar_wait(dfull + d, (uint32_t)((it / S::kBufs) & 1));
+                if (timed_out) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < NT; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(lane_base + (uint32_t)(d * NT + c), v);
+                    float4 sc[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[i] = reinterpret_cast<const float4 *>(xsc + d * NT + c)[i];
+                    tmem_wait_ld();
+                    const float *s = reinterpret_cast<const float *>(sc);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float s0 = s[2 * i] * wv, s1 = s[2 * i + 1] * wv;
+                        fma2_acc(acc[c / 2 + i], ((uint64_t)__float_as_uint(s1) << 32) | __float_as_uint(s0), v[2 * i],
+                                 v[2 * i + 1]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dempty + d);
+            }
+            auto value = [&](int c) {
+                return __uint_as_float((c & 1) ? (uint32_t)(acc[c >> 1] >> 32) : (uint32_t)acc[c >> 1]);
+            };
+            if (a.split == 1) {
+                if (n < a.N && !timed_out) {
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        if (c < t.rows) y[(int64_t)(t.row0 + c) * a.N + n] = round_to<Y>(value(c));
+                }
+            } else {
+                // column c is added and stored by CTA c / (NT / split); slot r holds CTA r's part
+                const int cols = NT / a.split;
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    const int to = c / cols, in = c - to * cols;
+                    st_cluster(map_rank(smem_u32(parts + ((int64_t)rank * cols + in) * kWRows + rl), (uint32_t)to),
+                               value(c));
+                }
+                fence_cluster();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int r = 0; r < a.split; ++r) arrive_cluster(map_rank(smem_u32(joined), (uint32_t)r));
+                }
+                timed_out |= !mbar_wait(joined, 0);
+                fence_cluster();
+                if (n < a.N && !timed_out) {
+                    for (int in = 0; in < cols; ++in) {
+                        const int c = rank * cols + in;
+                        if (c >= t.rows) break;
+                        float sum = 0.f;
+                        for (int r = 0; r < a.split; ++r) sum += parts[((int64_t)r * cols + in) * kWRows + rl];
+                        y[(int64_t)(t.row0 + c) * a.N + n] = round_to<Y>(sum);
+                    }
+                }
+            }
+        }
+    }
+    if (timed_out && a.status) atomicOr(a.status, Q4_STATUS_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    // a CTA of a cluster may go only when no other can still write to it
+    if (a.split > 1) cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, S::kCols);
+}
+
+// ---- host ---------------------------------------------------------------------------------
+bool encode_codes_map(CUtensorMap *tm, const uint8_t *codes, int64_t rows, int64_t K, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <int NT, typename Y>
+cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
+    using S = Stream<NT>;
+    // tiles: at most this many (which experts have rows is known on the device only)
+    const int64_t row_tiles = a.offsets ? std::min((int64_t)a.R, (int64_t)a.E + a.R / NT) : (a.R + NT - 1) / NT;
+    const int64_t tiles = row_tiles * a.nb;
+    // K is split over a cluster while the CTAs still fit on the machine at once, every CTA
+    // keeps two blocks of k or more, and each takes whole columns of the joined sums
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= sms && a.kb >= a.split * 4) a.split *= 2;
+    a.stages = (int)((kSmemMax - S::smem(0, a.split, a.E)) / (S::kStage + 16));
+    const int64_t blocks = (int64_t)((a.kb + a.split - 1) / a.split) * ((tiles + sms - 1) / sms);
+    a.stages = (int)std::max<int64_t>(2, std::min<int64_t>(std::min(a.stages, 16), blocks));
+    const size_t smem = S::smem(a.stages, a.split, a.E);
+    CUtensorMap tmx, tmw;
+    if (!encode_codes_map(&tmx, x, a.R, K, NT) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, kWRows))
+        return cudaErrorInvalidValue;
+    auto kern = fp8_stream<NT, Y>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : (tiles < sms ? tiles : sms)));
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)a.split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
+}
+
+template <typename Y>
+cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
+    // rows of a tile: the rows an expert has on average, doubled because experts differ
+    const int64_t typical = a.offsets ? std::min((int64_t)a.R, 2 * (((int64_t)a.R + a.E - 1) / a.E)) : a.R;
+    if (typical <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
+    if (typical <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
+    if (typical <= 64) return launch_stream<64, Y>(a, x, w, K, sms, st);
+    return launch_stream<128, Y>(a, x, w, K, sms, st);
+}
+
+int device_sms() {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms > 0 ? sms : 148;
+}
+
+q4_status fp8_product(const uint8_t *x, const float *xs, int64_t R, const int32_t *offsets, int64_t E, const uint8_t *w,
+                      const float *ws, int64_t N, int64_t K, void *y, q4_dtype yt, uint32_t *status, void *stream) {
+    if (yt != Q4_F32 && yt != Q4_BF16 && yt != Q4_F16) return Q4_ERR_ARG;
+    if (R < 0 || N < 0 || K < 1 || E < 0) return Q4_ERR_ARG;
+    // 32-bit row numbers; rows of codes are whole 16-byte units (TMA)
+    if (R > (1 << 30) || N > (1 << 30) || K > (1 << 30) || E > kMaxExperts || K % 16 != 0) return Q4_ERR_UNSUPPORTED;
+    if (E * N > INT32_MAX) return Q4_ERR_UNSUPPORTED;
+    if (R == 0 || N == 0 || E == 0) return Q4_OK;
+    if (!x || !xs || !w || !ws || !y) return Q4_ERR_ARG;
+    if ((uintptr_t)x % 16 || (uintptr_t)w % 16) return Q4_ERR_UNSUPPORTED;
+    Fp8Args a{xs, ws, offsets, y, status, N, (int32_t)R, (int32_t)E, (int32_t)((N + 127) / 128),
+              (int32_t)((K + 127) / 128), 1, 0};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int sms = device_sms();
+    const cudaError_t e = yt == Q4_F32    ? launch_fp8<float>(a, x, w, K, sms, st)
+                          : yt == Q4_BF16 ? launch_fp8<__nv_bfloat16>(a, x, w, K, sms, st)
+                                          : launch_fp8<__half>(a, x, w, K, sms, st);
+    return cuda_error(e, "fp8_gemm launch");
+}
+
+}  // namespace
+}  // namespace q4
+
+extern "C" {
+
+q4_status q4_fp8_gemm(const uint8_t *x, const float *xs, int64_t M, const uint8_t *w, const float *ws, int64_t N,
+                      int64_t K, void *y, q4_dtype yt, uint32_t *status_word, void *stream) {
+    return q4::fp8_product(x, xs, M, nullptr, 1, w, ws, N, K, y, yt, status_word, stream);
+}
+
+q4_status q4_fp8_gemm_grouped(const uint8_t *x, const float *xs, int64_t R, const int32_t *offsets, int64_t E,
+                              const uint8_t *w, const float *ws, int64_t N, int64_t K, void *y, q4_dtype yt,
+                              uint32_t *status_word, void *stream) {
+    if (!offsets && R > 0 && N > 0 && E > 0) return Q4_ERR_ARG;
+    return q4::fp8_product(x, xs, R, offsets, E, w, ws, N, K, y, yt, status_word, stream);
+}
+
+}  // extern "C"

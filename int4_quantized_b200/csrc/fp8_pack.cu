@@ -1,0 +1,327 @@
+// fp8_pack.cu -- e4m3 codes with one fp32 scale per block of 128, the format that the
+// block-scaled product of fp8_gemm.cu reads.
+//
+// The rule is qpack's with another code: per block, scale = fl32(max|v| / 448), 0 -> 1;
+// code = e4m3(fl32(v / scale)), to nearest, ties to even, at most 448 in magnitude. A block
+// is 128 consecutive values of a row (activations), or 128 rows x 128 columns (weights);
+// blocks at the right and lower edges hold what is left.
+//
+//   fp8_pack_rows   16 lanes take one block, 8 values each: one pass over x, the block's
+//                   maximum by four shuffles, one 8-byte store of codes a lane. Source rows
+//                   may be given by index (tokens sorted by expert on the way), and the
+//                   values may be silu(gate) * up of rows that hold gate and up side by side.
+//   fp8_pack_tiles  one CTA takes one 128 x 128 block, which stays in registers between the
+//                   maximum and the codes.
+// Both are bound by HBM: every value is read once and every code written once.
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace q4 {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr uint32_t kInf = 0x7f800000u;
+
+Q4_DEVINL float to_f32(float v) { return v; }
+Q4_DEVINL float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+Q4_DEVINL float to_f32(__half v) { return __half2float(v); }
+
+// 16 bytes of T as fp32 values.
+template <typename T>
+Q4_DEVINL void unpack16(const uint4 &r, float *v) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            v[i] = __uint_as_float(w[i]);
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// N consecutive values from p, `left` of them inside the row (zeros behind).
+template <typename T, int N, bool VEC>
+Q4_DEVINL void load_values(const T *p, int64_t left, float (&v)[N]) {
+    if constexpr (VEC) {
+        constexpr int PER = 16 / sizeof(T);
+        if (left > 0) {  // rows are whole 16-byte units here
+#pragma unroll
+            for (int i = 0; i < N / PER; ++i) unpack16<T>(reinterpret_cast<const uint4 *>(p)[i], v + i * PER);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
+    }
+}
+
+Q4_DEVINL uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+Q4_DEVINL float block_scale(uint32_t maxbits) {
+    const float s = __fdiv_rn(__uint_as_float(maxbits), kE4m3Max);
+    return s == 0.f ? 1.f : s;
+}
+
+// fl32(v / s) by the reciprocal and two residual corrections (P. Markstein, "IA-64 and
+// Elementary Functions", 2000: with y = RN(1/s) and a quotient within one ulp, one more
+// RN(q + RN-exact(v - q s) y) is the correctly rounded quotient; the first correction
+// brings RN(v y), up to two ulps off, within one). The residuals are exact while they stay
+// above the subnormal range: s >= 2^-90, and quotients below 2^-11, where they might not,
+// give the code 0 in any case. Other scales take the division itself. The residuals are
+// formed as q s - v so that v = -0 keeps its sign.
+struct BlockDiv {
+    float s, r;
+    bool fast;
+};
+Q4_DEVINL BlockDiv make_block_div(float s) {
+    BlockDiv d;
+    d.s = s;
+    d.fast = s >= 0x1p-90f && s <= 0x1p120f;
+    d.r = d.fast ? __frcp_rn(s) : 0.f;
+    return d;
+}
+Q4_DEVINL float quotient(const BlockDiv &d, float v) {
+    if (!d.fast) return __fdiv_rn(v, d.s);
+    const float q0 = __fmul_rn(v, d.r);
+    const float q1 = __fmaf_rn(-__fmaf_rn(q0, d.s, -v), d.r, q0);
+    return __fmaf_rn(-__fmaf_rn(q1, d.s, -v), d.r, q1);
+}
+Q4_DEVINL uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// silu(g) u = g u / (1 + exp(-g)), in fp32 with the hardware's exponential and reciprocal
+// (relative error at most (10 + 1.2 |g|) 2^-23; the code that follows keeps 4 bits). For
+// gates below about -88 the exponential is infinite and the value 0.
+Q4_DEVINL float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+struct RowsArgs {
+    const void *x;
+    const int32_t *rows;   // source row of each output row, or null
+    const int32_t *count;  // device count of output rows, or null
+    uint8_t *codes;
+    float *scales;
+    uint32_t *status;
+    int64_t x_rows, K, ldx;
+    uint32_t units, kb;  // blocks in all, blocks a row
+};
+
+template <typename T, bool SILU, bool VEC, int U>
+__global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
+    const int sub = threadIdx.x & 15;
+    const uint32_t first = blockIdx.x * (16 * U) + (threadIdx.x >> 4);
+    const int64_t live = a.count ? (int64_t)*a.count : INT64_MAX;
+    float v[U][8];
+    int64_t left[U];
+    uint32_t row[U], blk[U];
+    bool on[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        const uint32_t u = first + 16 * j;
+        on[j] = u < a.units;
+        row[j] = on[j] ? u / a.kb : 0;
+        blk[j] = on[j] ? u - row[j] * a.kb : 0;
+        int64_t src = row[j];
+        if (on[j] && a.rows) src = a.rows[row[j]];
+        on[j] = on[j] && src >= 0 && src < a.x_rows && (int64_t)row[j] < live;
+        const int64_t k0 = (int64_t)blk[j] * 128 + 8 * sub;
+        left[j] = on[j] ? a.K - k0 : 0;
+        const T *p = static_cast<const T *>(a.x) + (on[j] ? src * a.ldx + k0 : 0);
+        load_values<T, 8, VEC>(p, left[j], v[j]);
+        if constexpr (SILU) {
+            float up[8];
+            load_values<T, 8, VEC>(p + a.K, left[j], up);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = silu_mul(v[j][i], up[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[j][i]));
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!on[j]) continue;
+        const float s = block_scale(m);
+        const BlockDiv d = make_block_div(s);
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quotient(d, v[j][i]);
+        const uint32_t lo = e4m3x4(q[0], q[1], q[2], q[3]), hi = e4m3x4(q[4], q[5], q[6], q[7]);
+        uint8_t *c = a.codes + (int64_t)row[j] * a.K + (int64_t)blk[j] * 128 + 8 * sub;
+        if constexpr (VEC) {
+            if (left[j] > 0) *reinterpret_cast<uint2 *>(c) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left[j]) c[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        }
+        if (sub == 0) {
+            a.scales[(int64_t)row[j] * a.kb + blk[j]] = s;
+            if (m >= kInf && a.status) atomicOr(a.status, Q4_STATUS_NONFINITE);
+        }
+    }
+}
+
+// One 128 x 128 block of [.., N, K] weights a CTA. PER values a lane and load; a row's 128
+// columns are 128 / PER lanes wide, so 256 threads pass over the block in 64 / PER steps.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) fp8_pack_tiles(const T *__restrict__ w, int64_t N, int64_t K, uint32_t nb,
+                                                      uint32_t kb, uint8_t *__restrict__ codes,
+                                                      float *__restrict__ scales, uint32_t *status) {
+    constexpr int PER = 16 / sizeof(T), LANES = 128 / PER, ROWS = 256 / LANES, STEPS = 128 / ROWS;
+    const uint32_t t = blockIdx.x / kb, kblk = blockIdx.x - t * kb;  // t: (matrix, row block)
+    const uint32_t e = t / nb, nblk = t - e * nb;
+    const int64_t k0 = (int64_t)kblk * 128 + (threadIdx.x % LANES) * PER;
+    const int64_t n0 = (int64_t)nblk * 128 + threadIdx.x / LANES;
+    const T *src = w + (int64_t)e * N * K;
+    float v[STEPS][PER];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int64_t n = n0 + i * ROWS;
+        load_values<T, PER, VEC>(src + (n < N ? n * K + k0 : 0), n < N ? K - k0 : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) m = max(m, abs_bits(v[i][j]));
+    m = __reduce_max_sync(0xffffffffu, m);
+    __shared__ uint32_t part[8];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+    const float s = block_scale(m);
+    const BlockDiv d = make_block_div(s);
+    uint8_t *dst = codes + (int64_t)e * N * K;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int64_t n = n0 + i * ROWS;
+        if (n >= N) continue;
+        uint32_t c[PER / 4];
+#pragma unroll
+        for (int j = 0; j < PER / 4; ++j)
+            c[j] = e4m3x4(quotient(d, v[i][4 * j]), quotient(d, v[i][4 * j + 1]), quotient(d, v[i][4 * j + 2]),
+                          quotient(d, v[i][4 * j + 3]));
+        uint8_t *p = dst + n * K + k0;
+        if constexpr (VEC) {
+            if (k0 < K) {
+                if constexpr (PER == 8)
+                    *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
+                else
+                    *reinterpret_cast<uint32_t *>(p) = c[0];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (k0 + j < K) p[j] = (uint8_t)(c[j / 4] >> (8 * (j & 3)));
+        }
+    }
+    if (threadIdx.x == 0) {
+        scales[blockIdx.x] = s;
+        if (m >= kInf && status) atomicOr(status, Q4_STATUS_NONFINITE);
+    }
+}
+
+template <typename T>
+cudaError_t pack_rows(const RowsArgs &a, bool silu, cudaStream_t st) {
+    // whole 16-byte units a row: aligned loads of x and 8-byte stores of codes
+    const bool vec = a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.codes % 8 == 0 &&
+                     (a.ldx * (int64_t)sizeof(T)) % 16 == 0;
+    // four blocks a half warp keep the loads in flight that HBM needs; with fewer blocks than
+    // fill the machine so, one each (16 x 4096: 32 CTAs instead of 8)
+    const bool four = a.units >= 148 * 16 * 4;
+    const unsigned grid = (a.units + (four ? 63 : 15)) / (four ? 64 : 16);
+#define Q4_ROWS(S, V, U) fp8_pack_rows<T, S, V, U><<<grid, 256, 0, st>>>(a)
+    if (silu) {
+        if (vec) four ? Q4_ROWS(true, true, 4) : Q4_ROWS(true, true, 1);
+        else four ? Q4_ROWS(true, false, 4) : Q4_ROWS(true, false, 1);
+    } else {
+        if (vec) four ? Q4_ROWS(false, true, 4) : Q4_ROWS(false, true, 1);
+        else four ? Q4_ROWS(false, false, 4) : Q4_ROWS(false, false, 1);
+    }
+#undef Q4_ROWS
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pack_tiles(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *codes, float *scales, uint32_t *status,
+                       cudaStream_t st) {
+    const bool vec = (K * (int64_t)sizeof(T)) % 16 == 0 && (uintptr_t)w % 16 == 0 && (uintptr_t)codes % 8 == 0;
+    const uint32_t nb = (uint32_t)((N + 127) / 128), kb = (uint32_t)((K + 127) / 128);
+    const unsigned grid = (unsigned)(E * nb * kb);
+    if (vec)
+        fp8_pack_tiles<T, true><<<grid, 256, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
+    else
+        fp8_pack_tiles<T, false><<<grid, 256, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
+    return cudaGetLastError();
+}
+
+// Blocks of a call, at most 2^31 - 1 (such codes alone would be 275 GB).
+bool blocks_ok(int64_t rows, int64_t cols_blocks, int64_t *units) {
+    if (rows > 0 && cols_blocks > INT32_MAX / rows) return false;
+    *units = rows * cols_blocks;
+    return true;
+}
+
+}  // namespace
+}  // namespace q4
+
+extern "C" {
+
+q4_status q4_fp8_pack(const void *x, q4_dtype xt, int64_t x_rows, int64_t K, const int32_t *rows, int64_t R,
+                      const int32_t *count, uint32_t flags, uint8_t *codes, float *scales, uint32_t *status_word,
+                      void *stream) {
+    if (xt != Q4_F32 && xt != Q4_BF16 && xt != Q4_F16) return Q4_ERR_ARG;
+    if (flags & ~(uint32_t)Q4_FP8_PACK_SILU_MUL) return Q4_ERR_ARG;
+    if (x_rows < 0 || R < 0 || K < 1) return Q4_ERR_ARG;
+    if (!rows && R != x_rows) return Q4_ERR_ARG;
+    if (K > ((int64_t)1 << 30)) return Q4_ERR_UNSUPPORTED;
+    int64_t units;
+    if (!q4::blocks_ok(R, (K + 127) / 128, &units)) return Q4_ERR_UNSUPPORTED;
+    if (units == 0 || x_rows == 0) return Q4_OK;
+    if (!x || !codes || !scales) return Q4_ERR_ARG;
+    const bool silu = (flags & Q4_FP8_PACK_SILU_MUL) != 0;
+    q4::RowsArgs a{x, rows, count, codes, scales, status_word, x_rows, K, silu ? 2 * K : K, (uint32_t)units,
+                   (uint32_t)((K + 127) / 128)};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = xt == Q4_F32    ? q4::pack_rows<float>(a, silu, st)
+                          : xt == Q4_BF16 ? q4::pack_rows<__nv_bfloat16>(a, silu, st)
+                                          : q4::pack_rows<__half>(a, silu, st);
+    return q4::cuda_error(e, "fp8_pack launch");
+}
+
+q4_status q4_fp8_pack_weights(const void *w, q4_dtype wt, int64_t E, int64_t N, int64_t K, uint8_t *codes,
+                              float *scales, uint32_t *status_word, void *stream) {
+    if (wt != Q4_F32 && wt != Q4_BF16 && wt != Q4_F16) return Q4_ERR_ARG;
+    if (E < 0 || N < 0 || K < 1) return Q4_ERR_ARG;
+    if (N > ((int64_t)1 << 30) || K > ((int64_t)1 << 30)) return Q4_ERR_UNSUPPORTED;
+    int64_t tiles, all;
+    if (!q4::blocks_ok((N + 127) / 128, (K + 127) / 128, &tiles) || !q4::blocks_ok(E, tiles, &all))
+        return Q4_ERR_UNSUPPORTED;
+    if (all == 0) return Q4_OK;
+    if (!w || !codes || !scales) return Q4_ERR_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = wt == Q4_F32    ? q4::pack_tiles<float>(w, E, N, K, codes, scales, status_word, st)
+                          : wt == Q4_BF16 ? q4::pack_tiles<__nv_bfloat16>(w, E, N, K, codes, scales, status_word, st)
+                                          : q4::pack_tiles<__half>(w, E, N, K, codes, scales, status_word, st);
+    return q4::cuda_error(e, "fp8_pack_weights launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,157 @@
+"""Routed experts: tokens sorted by expert and back, the gradients, and a layer of experts
+with 8-bit weights.
+
+    tokens, pos, offsets = moe_sort(ids, E)       # ids: [T, k] expert of each choice
+    xs = moe_gather(x, tokens)                    # rows by expert
+    out = moe_combine(ys, pos, weights)           # out[t] = sum over j of weights[t, j] * ys[pos[t, j]]
+    dys, dweights = moe_combine_backward(dout, ys, pos, weights)
+    dx = moe_combine(dxs, pos)                    # the gradient of moe_gather
+
+    experts = Fp8Experts.pack(gate_up, down)      # [E, 2F, D] and [E, D, F] weights
+    out = experts(x, ids, weights)                # x: [T, D]
+
+The functions marshal arguments for libq4's q4_moe_* entry points (include/q4.h has the
+definitions); there is no CPU fallback.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _cuda, lib
+from .fp8 import E4M3, _arg, _blocks, _call, _dtype, fp8_gemm_grouped, fp8_pack, fp8_pack_weights
+
+
+def moe_sort(ids: torch.Tensor, num_experts: int) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Choices [T, k] (int32 or int64) -> (tokens [T * k], pos [T, k], offsets [E + 1]), int32.
+
+    Stable. An id outside 0 .. E - 1 drops its choice (pos = -1); tokens is -1 from
+    offsets[E] on.
+    """
+    _cuda(ids, "ids")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError("ids must be [T, k] with k >= 1")
+    T, k = ids.shape
+    E = int(num_experts)
+    if E < 1:
+        raise ValueError("num_experts must be at least 1")
+    dev = ids.device
+    # one allocation for the three
+    buf = torch.empty(2 * T * k + E + 1, dtype=torch.int32, device=dev)
+    tokens, pos, offsets = buf[:T * k], buf[T * k:2 * T * k].view(T, k), buf[2 * T * k:]
+    _call(dev, "moe_sort", lib().q4_moe_sort, ids.data_ptr(), 32 if ids.dtype == torch.int32 else 64, T, k, E,
+          tokens.data_ptr(), pos.data_ptr(), offsets.data_ptr())
+    return tokens, pos, offsets
+
+
+def moe_gather(x: torch.Tensor, tokens: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """xs[i] = x[tokens[i]] (x: [T, D]); entries outside 0 .. T - 1 leave row i as it was."""
+    _cuda(x, "x")
+    xt = _dtype(x.dtype, "x")
+    if x.dim() != 2 or x.shape[1] < 1 or tokens.dim() != 1:
+        raise ValueError("x must be [T, D] and tokens [R]")
+    dev = x.device
+    T, D = x.shape
+    R = tokens.shape[0]
+    if out is None:
+        out = torch.empty((R, D), dtype=x.dtype, device=dev)
+    _call(dev, "moe_gather", lib().q4_moe_gather, x.data_ptr(), xt, T, D, _arg(tokens, "tokens", torch.int32, None, dev),
+          R, _arg(out, "out", x.dtype, (R, D), dev))
+    return out
+
+
+def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = sum over j of weights[t, j] * ys[pos[t, j]] (ys: [R, D]; no weights: all ones)."""
+    _cuda(ys, "ys")
+    yt = _dtype(ys.dtype, "ys")
+    if ys.dim() != 2 or ys.shape[1] < 1 or pos.dim() != 2 or pos.shape[1] < 1:
+        raise ValueError("ys must be [R, D] and pos [T, k]")
+    dev = ys.device
+    R, D = ys.shape
+    T, k = pos.shape
+    if out is None:
+        out = torch.empty((T, D), dtype=ys.dtype, device=dev)
+    _call(dev, "moe_combine", lib().q4_moe_combine, ys.data_ptr(), yt, R, D, _arg(pos, "pos", torch.int32, None, dev),
+          _arg(weights, "weights", torch.float32, (T, k), dev), T, k, _arg(out, "out", ys.dtype, (T, D), dev))
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
+                         dys: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dys [R, D], dweights [T, k] fp32) of moe_combine for dout [T, D].
+
+    Rows of dys that pos does not name are left as they were (undefined where `dys` is not
+    given); the entries of pos inside 0 .. R - 1 must differ from one another.
+    """
+    _cuda(ys, "ys")
+    yt = _dtype(ys.dtype, "ys")
+    if ys.dim() != 2 or ys.shape[1] < 1 or pos.dim() != 2 or pos.shape[1] < 1:
+        raise ValueError("ys must be [R, D] and pos [T, k]")
+    if weights is None:
+        raise TypeError("weights must be a CUDA tensor")
+    dev = ys.device
+    R, D = ys.shape
+    T, k = pos.shape
+    if dys is None:
+        dys = torch.empty((R, D), dtype=ys.dtype, device=dev)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call(dev, "moe_combine_backward", lib().q4_moe_combine_backward, _arg(dout, "dout", ys.dtype, (T, D), dev),
+          ys.data_ptr(), yt, R, D, _arg(pos, "pos", torch.int32, None, dev),
+          _arg(weights, "weights", torch.float32, (T, k), dev), T, k, _arg(dys, "dys", ys.dtype, (R, D), dev),
+          dweights.data_ptr())
+    return dys, dweights
+
+
+class Fp8Experts:
+    """E gated MLPs with e4m3 weights: down[e] (silu(gate[e] x) * (up[e] x)) for the experts of each token.
+
+    gate_up [E, 2F, D] (the gate's rows, then up's) and down [E, D, F] are codes with scales
+    as fp8_pack_weights gives them (D and F multiples of 16). A call sorts the tokens by
+    expert, packs their rows in that order, multiplies, packs silu(gate) * up, multiplies and
+    adds the weighted answers: six kernels, nothing read back to the host.
+    """
+
+    def __init__(self, gate_up: torch.Tensor, gate_up_scales: torch.Tensor, down: torch.Tensor,
+                 down_scales: torch.Tensor):
+        _cuda(gate_up, "gate_up", E4M3)
+        if gate_up.dim() != 3 or gate_up.shape[1] % 2 or gate_up.shape[1] < 2:
+            raise ValueError("gate_up must be [E, 2F, D]")
+        E, F2, D = gate_up.shape
+        F = F2 // 2
+        if D % 16 or F % 16:
+            raise ValueError("D and F must be multiples of 16")
+        dev = gate_up.device
+        _arg(gate_up_scales, "gate_up_scales", torch.float32, (E, _blocks(F2), _blocks(D)), dev)
+        _arg(down, "down", E4M3, (E, D, F), dev)
+        _arg(down_scales, "down_scales", torch.float32, (E, _blocks(D), _blocks(F)), dev)
+        self.gate_up, self.gate_up_scales, self.down, self.down_scales = gate_up, gate_up_scales, down, down_scales
+        self.E, self.D, self.F = E, D, F
+
+    @classmethod
+    def pack(cls, gate_up: torch.Tensor, down: torch.Tensor) -> "Fp8Experts":
+        """From fp32, bf16 or fp16 weights [E, 2F, D] and [E, D, F]."""
+        return cls(*fp8_pack_weights(gate_up), *fp8_pack_weights(down))
+
+    def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """x [T, D], ids and weights [T, k] -> [T, D] of x's type.
+
+        A choice with an id outside 0 .. E - 1 adds nothing. status: one int32 that takes
+        Q4_STATUS_NONFINITE and Q4_STATUS_TIMEOUT.
+        """
+        _cuda(x, "x")
+        if x.dim() != 2 or x.shape[1] != self.D or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+            raise ValueError(f"x must be [T, {self.D}] and ids [T, k]")
+        if x.device != self.gate_up.device or ids.device != x.device:
+            raise ValueError(f"x and ids must be on {self.gate_up.device}")
+        tokens, pos, offsets = moe_sort(ids, self.E)
+        live = offsets[self.E:]  # rows that have an expert
+        xq, xs = fp8_pack(x, rows=tokens, status=status)
+        h = fp8_gemm_grouped(xq, xs, self.gate_up, self.gate_up_scales, offsets, out_dtype=x.dtype, status=status)
+        hq, hs = fp8_pack(h, count=live, silu_mul=True, status=status)
+        ys = fp8_gemm_grouped(hq, hs, self.down, self.down_scales, offsets, out_dtype=x.dtype, status=status)
+        return moe_combine(ys, pos, weights)
