@@ -15,6 +15,16 @@
 //   warp 1      tensor memory, MMA issue (4 instructions of 32 k a block)
 //   warp 2      the rows' scales of each block, by 4-byte asynchronous copies
 //   warps 4-7   promotion and stores; lane = weight row, so stores of y are contiguous
+//
+// Many rows (fp8_wide): a pair of CTAs (cta_group::2) makes one tile of 256 rows of x x BN
+// weight rows. Each CTA loads its own 128 rows of x and half of the weights, so a block of k
+// costs each SM 128 + BN / 2 rows of 128 bytes instead of 128 + BN: at 256 x 256 a single CTA
+// would have to bring 96 bytes a clock from L2, above the 64 an SM can take. Here D's lanes
+// are rows of x, so that the scale of a thread's whole row of D is one number a block of k.
+//   warp 0      TMA producer (both CTAs; all bytes are counted on the first CTA's barriers)
+//   warp 1      tensor memory; in the first CTA, MMA issue for both
+//   warps 4-11  promotion and stores: 32 rows x BN / 2 columns a warp, kept in registers;
+//               the first four warps give theirs up to them (setmaxnreg)
 // Every wait is bounded (about one second); one that gives up sets Q4_STATUS_TIMEOUT in the
 // status word, and the roles run to completion without further waits.
 #include <cuda.h>
@@ -85,22 +95,23 @@ Q4_DEVINL void count_tiles(const Fp8Args &a, int tile_rows, int32_t *first, int3
 }
 
 struct Tile {
-    int e, nb;       // expert, weight block
+    int e, nb;       // expert, column tile
     int row0, rows;  // rows of x
 };
-// Tile j of first[E] * nb: by expert, then weight block, then row tile, so that the row tiles
-// that share weights come one after the other and find them in L2.
-Q4_DEVINL Tile tile_at(const Fp8Args &a, int tile_rows, const int32_t *first, const int32_t *rows0, int64_t j) {
-    // the expert: the last e with first[e] * nb <= j
+// Tile j of first[E] * cols (cols: column tiles of a matrix): by expert, then column tile, then
+// row tile, so that the row tiles that share weights come one after the other and find them
+// in L2.
+Q4_DEVINL Tile tile_at(const Fp8Args &a, int tile_rows, int cols, const int32_t *first, const int32_t *rows0, int64_t j) {
+    // the expert: the last e with first[e] * cols <= j
     int lo = 0, hi = a.E;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)first[mid] * a.nb <= j) lo = mid;
+        if ((int64_t)first[mid] * cols <= j) lo = mid;
         else hi = mid;
     }
     // several experts without rows share a first tile: the last of them is the one with rows
     const int n = first[lo + 1] - first[lo];
-    const int64_t i = j - (int64_t)first[lo] * a.nb;
+    const int64_t i = j - (int64_t)first[lo] * cols;
     Tile t;
     t.e = lo;
     t.nb = (int)(i / n);
@@ -131,6 +142,12 @@ Q4_DEVINL void st_cluster(uint32_t addr, float v) {
 }
 Q4_DEVINL void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// An arrival that publishes no memory of its own: the buffers of tensor memory it frees are
+// ordered by the tcgen05 fences. (With release at cluster scope each arrival waited for the
+// thread's outstanding loads: 31 % of the epilogue warps' time.)
+Q4_DEVINL void arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 Q4_DEVINL void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 Q4_DEVINL void cluster_sync_all() {
@@ -212,7 +229,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
         if (lane == 0) {
             int it = 0;
             for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
-                const Tile t = tile_at(a, NT, first, rows0, j);
+                const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
                 const int wrow = (int)(t.e * a.N + (int64_t)t.nb * kWRows);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int s = it % a.stages;
@@ -253,7 +270,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     } else if (warp == 2) {
         int it = 0;
         for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
-            const Tile t = tile_at(a, NT, first, rows0, j);
+            const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
             for (int kb = k0; kb < k1; ++kb, ++it) {
                 const int d = it % S::kBufs;
                 if (it >= S::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / S::kBufs - 1) & 1));
@@ -275,7 +292,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
         Y *const y = static_cast<Y *>(a.y);
         int it = 0;
         for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
-            const Tile t = tile_at(a, NT, first, rows0, j);
+            const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
             const float *wsc = a.ws + ((int64_t)t.e * a.nb + t.nb) * a.kb;
             const int64_t n = (int64_t)t.nb * kWRows + rl;
             uint64_t acc[NT / 2];
@@ -357,6 +374,210 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     if (warp == 1) tmem_dealloc(tmem, S::kCols);
 }
 
+// ---- many rows ----------------------------------------------------------------------------
+constexpr int kWideRows = 256;     // rows of x a pair
+constexpr int kWideThreads = 384;  // TMA, MMA, two without a role, eight epilogue warps
+// The block launches with 168 registers a thread; the first warpgroup keeps 72, the two
+// epilogue warpgroups (128 fp32 sums a thread) take 216: 128 * 72 + 256 * 216 is exactly the
+// 384 * 168 that the block holds, so every increase is served.
+constexpr int kWideRegs = 168, kWideLow = 72, kWideHigh = 216;
+static_assert(128 * kWideLow + 256 * kWideHigh == kWideThreads * kWideRegs, "register split");
+
+template <int BN>
+struct Wide {
+    static constexpr int kXBytes = 128 * kBK;
+    static constexpr int kBBytes = BN / 2 * kBK;
+    static constexpr int kStage = kXBytes + kBBytes;
+    static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 8 of 24 KB
+    static constexpr int kBufs = 512 / BN;           // all 512 columns of tensor memory
+    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kWideRows >> 4) << 24);
+    static size_t smem(int E) {
+        return 1024 + (size_t)kStages * kStage + (2 * kStages + 2 * kBufs + 1) * 8 + 16 + (size_t)(2 * E + 2) * 4;
+    }
+};
+
+// 32 bytes in one store: a whole sector, although neighbouring lanes write different rows.
+Q4_DEVINL void st_v8(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+template <typename Y>
+Q4_DEVINL uint32_t two(float lo, float hi) {
+    if constexpr (std::is_same<Y, __half>::value) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+template <int BN, typename Y>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw) {
+    using W = Wide<BN>;
+    constexpr int HALF = BN / 2;  // columns an epilogue warp keeps
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + W::kStages * W::kStage);
+    uint64_t *empty = full + W::kStages;
+    uint64_t *dfull = empty + W::kStages;
+    uint64_t *dempty = dfull + W::kBufs;
+    uint64_t *done = dempty + W::kBufs;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 4);
+    int32_t *rows0 = first + a.E + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < W::kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < W::kBufs; ++i) {
+            mbar_init(dfull + i, 1);
+            mbar_init(dempty + i, 16);  // the epilogue warps of both CTAs
+        }
+        mbar_init(done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc2(tmem_slot, 512);
+        tmem_relinquish2();
+    }
+    count_tiles(a, kWideRows, first, rows0);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int cols = (int)((a.N + BN - 1) / BN);
+    const int64_t tiles = (int64_t)first[a.E] * cols, step = gridDim.x / 2;
+    bool timed_out = false;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLow));
+        if (warp == 0 && lane == 0) {
+            int it = 0;
+            for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
+                const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
+                const int wrow = (int)(t.e * a.N + (int64_t)t.nb * BN + rank * HALF);
+                const int xrow = t.row0 + rank * 128;
+                for (int kb = 0; kb < a.kb; ++kb, ++it) {
+                    const int s = it % W::kStages;
+                    if (it >= W::kStages) timed_out = !mbar_wait(empty + s, (uint32_t)((it / W::kStages - 1) & 1));
+                    if (timed_out) break;
+                    // the first CTA's barrier counts the bytes of both
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * W::kStage);
+                    const uint32_t bar = map_rank(smem_u32(full + s), 0);
+                    uint8_t *st = ring + s * W::kStage;
+                    tma_load_2d_pair(st, &tmx, bar, kb * kBK, xrow);
+                    tma_load_2d_pair(st + W::kXBytes, &tmw, bar, kb * kBK, wrow);
+                }
+            }
+            // no copy may land after the pair has gone
+            if (rank == 0)
+                for (int i = max(0, it - W::kStages); i < it; ++i)
+                    timed_out |= !mbar_wait(full + i % W::kStages, (uint32_t)((i / W::kStages) & 1));
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            int it = 0;
+            for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
+                for (int kb = 0; kb < a.kb; ++kb, ++it) {
+                    const int s = it % W::kStages, d = it % W::kBufs;
+                    if (it >= W::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / W::kBufs - 1) & 1));
+                    if (!timed_out) timed_out = !mbar_wait(full + s, (uint32_t)((it / W::kStages) & 1));
+                    if (timed_out) break;
+                    tc_fence_after();
+                    const uint8_t *st = ring + s * W::kStage;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 32; ++kk)
+                        umma_f8_pair(tmem + (uint32_t)(d * BN), sw128_desc(st + kk * 32),
+                                     sw128_desc(st + W::kXBytes + kk * 32), W::kIdesc, kk > 0 ? 1u : 0u);
+                    umma_commit_pair(empty + s);
+                    umma_commit_pair(dfull + d);
+                }
+            }
+            umma_commit_pair(done);
+            timed_out |= !mbar_wait(done, 0);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideHigh));
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * HALF);
+        Y *const y = static_cast<Y *>(a.y);
+        constexpr int PER = 32 / (int)sizeof(Y);  // values a 32-byte store
+        const bool vec = a.N % PER == 0 && (uintptr_t)a.y % 32 == 0;
+        int it = 0;
+        for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
+            const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
+            const int rl = rank * 128 + 32 * q + lane;  // row inside the tile
+            const bool live = rl < t.rows;
+            const int64_t n0 = (int64_t)t.nb * BN + half * HALF;
+            const float *xsc = a.xs + (int64_t)(t.row0 + min(rl, t.rows - 1)) * a.kb;
+            const float *wsc = a.ws + ((int64_t)t.e * a.nb + min((int)(n0 / 128), a.nb - 1)) * a.kb;
+            uint64_t acc[HALF / 2];
+#pragma unroll
+            for (int i = 0; i < HALF / 2; ++i) acc[i] = 0ull;
+            float x_next = xsc[0], w_next = wsc[0];
+            for (int kb = 0; kb < a.kb; ++kb, ++it) {
+                const int d = it % W::kBufs;
+                const float sc = x_next * w_next;
+                const uint64_t s2 = ((uint64_t)__float_as_uint(sc) << 32) | __float_as_uint(sc);
+                if (kb + 1 < a.kb) x_next = xsc[kb + 1], w_next = wsc[kb + 1];
+                timed_out = !mbar_wait(dfull + d, (uint32_t)((it / W::kBufs) & 1));
+                if (timed_out) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < HALF; c += 32) {
+                    uint32_t v0[16], v1[16];
+                    tmem_ld16(lane_base + (uint32_t)(d * BN + c), v0);
+                    tmem_ld16(lane_base + (uint32_t)(d * BN + c + 16), v1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        fma2_acc(acc[c / 2 + i], s2, v0[2 * i], v0[2 * i + 1]);
+                        fma2_acc(acc[c / 2 + 8 + i], s2, v1[2 * i], v1[2 * i + 1]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_peer(map_rank(smem_u32(dempty + d), 0));
+            }
+            if (!live || timed_out) continue;
+            auto value = [&](int c) {
+                return __uint_as_float((c & 1) ? (uint32_t)(acc[c >> 1] >> 32) : (uint32_t)acc[c >> 1]);
+            };
+            Y *yr = y + (int64_t)(t.row0 + rl) * a.N + n0;
+            if (vec) {
+#pragma unroll
+                for (int c = 0; c < HALF; c += PER) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if constexpr (sizeof(Y) == 4) v[i] = __float_as_uint(value(c + i));
+                        else v[i] = two<Y>(value(c + 2 * i), value(c + 2 * i + 1));
+                    }
+                    if (n0 + c < a.N) st_v8(yr + c, v);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < HALF; ++c)
+                    if (n0 + c < a.N) yr[c] = round_to<Y>(value(c));
+            }
+        }
+    }
+    if (timed_out && a.status) atomicOr(a.status, Q4_STATUS_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA goes while the other may still reach into it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc2(tmem, 512);
+}
+
 // ---- host ---------------------------------------------------------------------------------
 bool encode_codes_map(CUtensorMap *tm, const uint8_t *codes, int64_t rows, int64_t K, int box_rows) {
     EncodeTiledFn enc = encode_fn();
@@ -406,6 +627,29 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
 }
 
+template <int BN, typename Y>
+cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
+    using W = Wide<BN>;
+    const int64_t row_tiles = a.offsets ? std::min((int64_t)a.R, (int64_t)a.E + a.R / kWideRows)
+                                        : (a.R + kWideRows - 1) / kWideRows;
+    const int64_t tiles = row_tiles * ((a.N + BN - 1) / BN);
+    CUtensorMap tmx, tmw;
+    if (!encode_codes_map(&tmx, x, a.R, K, 128) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, BN / 2))
+        return cudaErrorInvalidValue;
+    auto kern = fp8_wide<BN, Y>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    if (e != cudaSuccess) return e;
+    // the register split assumes the block launches at exactly kWideRegs a thread; any other
+    // allocation could leave an increase waiting: refuse to launch
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kWideRegs) return cudaErrorInvalidConfiguration;
+    const unsigned pairs = (unsigned)std::min<int64_t>(tiles, sms / 2);
+    kern<<<2 * pairs, kWideThreads, W::smem(a.E), st>>>(a, tmx, tmw);
+    return cudaGetLastError();
+}
+
 template <typename Y>
 cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     // rows of a tile: the rows an expert has on average, doubled because experts differ
@@ -413,7 +657,8 @@ cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int
     if (typical <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
     if (typical <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
     if (typical <= 64) return launch_stream<64, Y>(a, x, w, K, sms, st);
-    return launch_stream<128, Y>(a, x, w, K, sms, st);
+    if (typical <= 128) return launch_stream<128, Y>(a, x, w, K, sms, st);
+    return launch_wide<256, Y>(a, x, w, K, sms, st);
 }
 
 int device_sms() {
