@@ -14,7 +14,7 @@
 //   warp 0      TMA producer: 128 x 128 weights and NT x 128 codes of x a block of k
 //   warp 1      tensor memory, MMA issue (4 instructions of 32 k a block)
 //   warp 2      the rows' scales of each block, by 4-byte asynchronous copies
-//   warps 4-7   promotion and stores; lane = weight row, so stores of y are contiguous
+//   warps 4-..  promotion and stores; lane = weight row, so stores of y are contiguous
 //
 // Many rows (fp8_wide): a pair of CTAs (cta_group::2) makes one tile of 256 rows of x x BN
 // weight rows. Each CTA loads its own 128 rows of x and half of the weights, so a block of k
@@ -120,6 +120,18 @@ Q4_DEVINL Tile tile_at(const Fp8Args &a, int tile_rows, int cols, const int32_t 
     return t;
 }
 
+// A place in a ring of n slots and the parity of its round, kept without divisions.
+struct Slot {
+    int i = 0;
+    uint32_t round = 0;
+    Q4_DEVINL void next(int n) {
+        if (++i == n) {
+            i = 0;
+            round ^= 1;
+        }
+    }
+};
+
 template <typename Y>
 Q4_DEVINL Y round_to(float v) {
     if constexpr (std::is_same<Y, float>::value) return v;
@@ -147,7 +159,7 @@ Q4_DEVINL void arrive_cluster(uint32_t bar) {
 // ordered by the tcgen05 fences. (With release at cluster scope each arrival waited for the
 // thread's outstanding loads: 31 % of the epilogue warps' time.)
 Q4_DEVINL void arrive_peer(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 Q4_DEVINL void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 Q4_DEVINL void cluster_sync_all() {
@@ -155,13 +167,18 @@ Q4_DEVINL void cluster_sync_all() {
 }
 
 // ---- few rows ---------------------------------------------------------------------------
-constexpr int kStreamThreads = 256;
 template <int NT>
 struct Stream {
     static constexpr int kXBytes = NT * kBK;
     static constexpr int kStage = kWBytes + kXBytes;
-    static constexpr int kBufs = NT <= 32 ? 8 : 256 / NT;  // tensor-memory buffers of NT columns
-    static constexpr int kCols = kBufs * NT;               // 128 or 256 of the 512 columns
+    static constexpr int kBufs = NT <= 64 ? 8 : 4;       // tensor-memory buffers of NT columns
+    static constexpr int kCols = kBufs * NT;             // 128 to 512 columns
+    // one warp an SM quarter adds up to 32 columns a block of k before the next block's sums
+    // are there; wider tiles take two (NT = 128 with one: 0.9 us a block, its loads and waits
+    // one after the other)
+    static constexpr int kEpiWarps = NT <= 32 ? 4 : 8;
+    static constexpr int kOwn = NT * 4 / kEpiWarps;      // columns a warp keeps
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kWRows >> 4) << 24);
     // ring, exchange buffer of the split sums, scales, barriers
     static size_t smem(int stages, int split, int E) {
@@ -171,7 +188,7 @@ struct Stream {
 };
 
 template <int NT, typename Y>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+__global__ void __launch_bounds__(Stream<NT>::kThreads, 1)
 fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw) {
     using S = Stream<NT>;
     extern __shared__ uint8_t smem_raw[];
@@ -199,11 +216,11 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
         }
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(dfull + i, 1);
-            mbar_init(dempty + i, 4);
+            mbar_init(dempty + i, S::kEpiWarps);
             mbar_init(sfull + i, 32);
         }
         mbar_init(done, 1);
-        mbar_init(joined, 4 * a.split);
+        mbar_init(joined, S::kEpiWarps * a.split);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -227,105 +244,120 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            Slot s;
+            int filled = 0;
             for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
                 const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
                 const int wrow = (int)(t.e * a.N + (int64_t)t.nb * kWRows);
-                for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = it % a.stages;
-                    if (it >= a.stages) timed_out = !mbar_wait(empty + s, (uint32_t)((it / a.stages - 1) & 1));
+                for (int kb = k0; kb < k1; ++kb) {
+                    // a slot that was never filled counts as freed in the round before
+                    timed_out = !mbar_wait(empty + s.i, s.round ^ 1);
                     if (timed_out) break;
-                    uint8_t *st = ring + (size_t)s * S::kStage;
-                    mbar_arrive_expect_tx(full + s, S::kStage);
-                    tma_load_2d(st, &tmw, full + s, kb * kBK, wrow);
-                    tma_load_2d(st + kWBytes, &tmx, full + s, kb * kBK, t.row0);
+                    uint8_t *st = ring + (size_t)s.i * S::kStage;
+                    mbar_arrive_expect_tx(full + s.i, S::kStage);
+                    tma_load_2d(st, &tmw, full + s.i, kb * kBK, wrow);
+                    tma_load_2d(st + kWBytes, &tmx, full + s.i, kb * kBK, t.row0);
+                    s.next(a.stages);
+                    filled = min(filled + 1, a.stages);
                 }
             }
-            // no copy may land after the block has gone
-            for (int i = max(0, it - a.stages); i < it; ++i)
-                timed_out |= !mbar_wait(full + i % a.stages, (uint32_t)((i / a.stages) & 1));
+            // no copy may land after the block has gone: the slots' last rounds
+            for (int i = 0; i < filled; ++i)
+                timed_out |= !mbar_wait(full + i, i < s.i ? s.round : s.round ^ 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0;
-            for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
-                for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = it % a.stages, d = it % S::kBufs;
-                    if (it >= S::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / S::kBufs - 1) & 1));
-                    if (!timed_out) timed_out = !mbar_wait(full + s, (uint32_t)((it / a.stages) & 1));
-                    if (timed_out) break;
-                    tc_fence_after();
-                    const uint8_t *st = ring + (size_t)s * S::kStage;
+        // the whole warp keeps step and one lane issues: operands stay uniform across the warp
+        Slot s, d;
+        const uint64_t base = sw128_desc(ring);
+        const uint32_t dt = __shfl_sync(0xffffffffu, tmem, 0);
+        for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+            for (int kb = k0; kb < k1; ++kb) {
+                timed_out = !mbar_wait(dempty + d.i, d.round ^ 1);
+                if (!timed_out) timed_out = !mbar_wait(full + s.i, s.round);
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                tc_fence_after();
+                const uint64_t wd = base + (uint32_t)(s.i * (S::kStage >> 4)), xd = wd + (kWBytes >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk)
-                        umma_f8(tmem + (uint32_t)(d * NT), sw128_desc(st + kk * 32), sw128_desc(st + kWBytes + kk * 32),
-                                S::kIdesc, kk > 0 ? 1u : 0u);
-                    umma_commit(empty + s);
-                    umma_commit(dfull + d);
+                        umma_f8(dt + (uint32_t)(d.i * NT), wd + 2 * kk, xd + 2 * kk, S::kIdesc, kk > 0 ? 1u : 0u);
+                    umma_commit(empty + s.i);
+                    umma_commit(dfull + d.i);
                 }
+                __syncwarp();
+                s.next(a.stages);
+                d.next(S::kBufs);
             }
-            umma_commit(done);
-            timed_out |= !mbar_wait(done, 0);
         }
+        if (elect_one()) umma_commit(done);
+        __syncwarp();
+        timed_out |= !mbar_wait(done, 0);
     } else if (warp == 2) {
-        int it = 0;
+        Slot d;
         for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
             const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
-            for (int kb = k0; kb < k1; ++kb, ++it) {
-                const int d = it % S::kBufs;
-                if (it >= S::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / S::kBufs - 1) & 1));
+            for (int kb = k0; kb < k1; ++kb) {
+                timed_out = !mbar_wait(dempty + d.i, d.round ^ 1);
                 if (timed_out) break;
 #pragma unroll
                 for (int c = 0; c < NT; c += 32) {
                     const int col = c + lane;
                     if (col < NT)
-                        cp_async4(xsc + d * NT + col,
+                        cp_async4(xsc + d.i * NT + col,
                                   a.xs + (int64_t)(t.row0 + min(col, t.rows - 1)) * a.kb + kb);
                 }
-                cp_async_arrive(sfull + d);
+                cp_async_arrive(sfull + d.i);
+                d.next(S::kBufs);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= 4) {
-        const int q = warp & 3, rl = 32 * q + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+        constexpr int OWN = S::kOwn;
+        const int q = warp & 3, rl = 32 * q + lane, c0 = ((warp - 4) >> 2) * OWN;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)c0;
         Y *const y = static_cast<Y *>(a.y);
-        int it = 0;
+        Slot d;
         for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
             const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
             const float *wsc = a.ws + ((int64_t)t.e * a.nb + t.nb) * a.kb;
             const int64_t n = (int64_t)t.nb * kWRows + rl;
-            uint64_t acc[NT / 2];
+            uint64_t acc[OWN / 2];
 #pragma unroll
-            for (int i = 0; i < NT / 2; ++i) acc[i] = 0ull;
+            for (int i = 0; i < OWN / 2; ++i) acc[i] = 0ull;
             float w_next = k0 < k1 ? wsc[k0] : 0.f;
-            for (int kb = k0; kb < k1; ++kb, ++it) {
-                const int d = it % S::kBufs;
+            for (int kb = k0; kb < k1; ++kb) {
                 const float wv = w_next;
                 if (kb + 1 < k1) w_next = wsc[kb + 1];
-                timed_out = !mbar_wait(sfull + d, (uint32_t)((it / S::kBufs) & 1));
-                if (!timed_out) timed_out = !mbar_wait(dfull + d, (uint32_t)((it / S::kBufs) & 1));
+                timed_out = !mbar_wait(sfull + d.i, d.round);
+                if (!timed_out) timed_out = !mbar_wait(dfull + d.i, d.round);
                 if (timed_out) break;
                 tc_fence_after();
+                constexpr int CH = OWN < 32 ? OWN : 32;
 #pragma unroll
-                for (int c = 0; c < NT; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(lane_base + (uint32_t)(d * NT + c), v);
-                    float4 sc[4];
+                for (int c = 0; c < OWN; c += CH) {
+                    uint32_t v[CH];
+                    if constexpr (CH == 32) tmem_ld32(lane_base + (uint32_t)(d.i * NT + c), v);
+                    else tmem_ld16(lane_base + (uint32_t)(d.i * NT + c), v);
+                    // the columns' scales while the sums are on their way
+                    float s[CH];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[i] = reinterpret_cast<const float4 *>(xsc + d * NT + c)[i];
-                    tmem_wait_ld();
-                    const float *s = reinterpret_cast<const float *>(sc);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float s0 = s[2 * i] * wv, s1 = s[2 * i + 1] * wv;
-                        fma2_acc(acc[c / 2 + i], ((uint64_t)__float_as_uint(s1) << 32) | __float_as_uint(s0), v[2 * i],
-                                 v[2 * i + 1]);
+                    for (int i = 0; i < CH / 4; ++i) {
+                        const float4 f = reinterpret_cast<const float4 *>(xsc + d.i * NT + c0 + c)[i];
+                        s[4 * i] = f.x * wv, s[4 * i + 1] = f.y * wv, s[4 * i + 2] = f.z * wv, s[4 * i + 3] = f.w * wv;
                     }
+                    tmem_wait_ld();
+                    if (c + CH == OWN) {  // all read: the buffer and its scales are free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(dempty + d.i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < CH / 2; ++i)
+                        fma2_acc(acc[c / 2 + i], ((uint64_t)__float_as_uint(s[2 * i + 1]) << 32) | __float_as_uint(s[2 * i]),
+                                 v[2 * i], v[2 * i + 1]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(dempty + d);
+                d.next(S::kBufs);
             }
             auto value = [&](int c) {
                 return __uint_as_float((c & 1) ? (uint32_t)(acc[c >> 1] >> 32) : (uint32_t)acc[c >> 1]);
@@ -333,15 +365,15 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
             if (a.split == 1) {
                 if (n < a.N && !timed_out) {
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        if (c < t.rows) y[(int64_t)(t.row0 + c) * a.N + n] = round_to<Y>(value(c));
+                    for (int c = 0; c < OWN; ++c)
+                        if (c0 + c < t.rows) y[(int64_t)(t.row0 + c0 + c) * a.N + n] = round_to<Y>(value(c));
                 }
             } else {
                 // column c is added and stored by CTA c / (NT / split); slot r holds CTA r's part
                 const int cols = NT / a.split;
 #pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    const int to = c / cols, in = c - to * cols;
+                for (int c = 0; c < OWN; ++c) {
+                    const int to = (c0 + c) / cols, in = c0 + c - to * cols;
                     st_cluster(map_rank(smem_u32(parts + ((int64_t)rank * cols + in) * kWRows + rl), (uint32_t)to),
                                value(c));
                 }
@@ -353,7 +385,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
                 timed_out |= !mbar_wait(joined, 0);
                 fence_cluster();
                 if (n < a.N && !timed_out) {
-                    for (int in = 0; in < cols; ++in) {
+                    for (int in = (warp - 4) >> 2; in < cols; in += S::kEpiWarps / 4) {
                         const int c = rank * cols + in;
                         if (c >= t.rows) break;
                         float sum = 0.f;
@@ -460,47 +492,59 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideLow));
-        if (warp == 0 && lane == 0) {
-            int it = 0;
-            for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
-                const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
-                const int wrow = (int)(t.e * a.N + (int64_t)t.nb * BN + rank * HALF);
-                const int xrow = t.row0 + rank * 128;
-                for (int kb = 0; kb < a.kb; ++kb, ++it) {
-                    const int s = it % W::kStages;
-                    if (it >= W::kStages) timed_out = !mbar_wait(empty + s, (uint32_t)((it / W::kStages - 1) & 1));
-                    if (timed_out) break;
-                    // the first CTA's barrier counts the bytes of both
-                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * W::kStage);
-                    const uint32_t bar = map_rank(smem_u32(full + s), 0);
-                    uint8_t *st = ring + s * W::kStage;
-                    tma_load_2d_pair(st, &tmx, bar, kb * kBK, xrow);
-                    tma_load_2d_pair(st + W::kXBytes, &tmw, bar, kb * kBK, wrow);
+        if (warp == 0) {
+            if (lane == 0) {
+                Slot s;
+                int filled = 0;
+                for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
+                    const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
+                    const int wrow = (int)(t.e * a.N + (int64_t)t.nb * BN + rank * HALF);
+                    const int xrow = t.row0 + rank * 128;
+                    for (int kb = 0; kb < a.kb; ++kb) {
+                        timed_out = !mbar_wait(empty + s.i, s.round ^ 1);
+                        if (timed_out) break;
+                        // the first CTA's barrier counts the bytes of both
+                        if (rank == 0) mbar_arrive_expect_tx(full + s.i, 2 * W::kStage);
+                        const uint32_t bar = map_rank(smem_u32(full + s.i), 0);
+                        uint8_t *st = ring + s.i * W::kStage;
+                        tma_load_2d_pair(st, &tmx, bar, kb * kBK, xrow);
+                        tma_load_2d_pair(st + W::kXBytes, &tmw, bar, kb * kBK, wrow);
+                        s.next(W::kStages);
+                        filled = min(filled + 1, W::kStages);
+                    }
                 }
+                // no copy may land after the pair has gone: the slots' last rounds
+                if (rank == 0)
+                    for (int i = 0; i < filled; ++i)
+                        timed_out |= !mbar_wait(full + i, i < s.i ? s.round : s.round ^ 1);
             }
-            // no copy may land after the pair has gone
-            if (rank == 0)
-                for (int i = max(0, it - W::kStages); i < it; ++i)
-                    timed_out |= !mbar_wait(full + i % W::kStages, (uint32_t)((i / W::kStages) & 1));
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            int it = 0;
+        } else if (warp == 1 && rank == 0) {
+            // the whole warp keeps step and one lane issues: operands stay uniform across the warp
+            Slot s, d;
+            const uint64_t base = sw128_desc(ring);
+            const uint32_t dt = __shfl_sync(0xffffffffu, tmem, 0);
             for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
-                for (int kb = 0; kb < a.kb; ++kb, ++it) {
-                    const int s = it % W::kStages, d = it % W::kBufs;
-                    if (it >= W::kBufs) timed_out = !mbar_wait(dempty + d, (uint32_t)((it / W::kBufs - 1) & 1));
-                    if (!timed_out) timed_out = !mbar_wait(full + s, (uint32_t)((it / W::kStages) & 1));
+                for (int kb = 0; kb < a.kb; ++kb) {
+                    timed_out = !mbar_wait(dempty + d.i, d.round ^ 1);
+                    if (!timed_out) timed_out = !mbar_wait(full + s.i, s.round);
+                    timed_out = __any_sync(0xffffffffu, timed_out);
                     if (timed_out) break;
                     tc_fence_after();
-                    const uint8_t *st = ring + s * W::kStage;
+                    const uint64_t xd = base + (uint32_t)(s.i * (W::kStage >> 4)), wd = xd + (W::kXBytes >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 32; ++kk)
-                        umma_f8_pair(tmem + (uint32_t)(d * BN), sw128_desc(st + kk * 32),
-                                     sw128_desc(st + W::kXBytes + kk * 32), W::kIdesc, kk > 0 ? 1u : 0u);
-                    umma_commit_pair(empty + s);
-                    umma_commit_pair(dfull + d);
+                        for (int kk = 0; kk < kBK / 32; ++kk)
+                            umma_f8_pair(dt + (uint32_t)(d.i * BN), xd + 2 * kk, wd + 2 * kk, W::kIdesc, kk > 0 ? 1u : 0u);
+                        umma_commit_pair(empty + s.i);
+                        umma_commit_pair(dfull + d.i);
+                    }
+                    __syncwarp();
+                    s.next(W::kStages);
+                    d.next(W::kBufs);
                 }
             }
-            umma_commit_pair(done);
+            if (elect_one()) umma_commit_pair(done);
+            __syncwarp();
             timed_out |= !mbar_wait(done, 0);
         }
     } else {
@@ -510,7 +554,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
         Y *const y = static_cast<Y *>(a.y);
         constexpr int PER = 32 / (int)sizeof(Y);  // values a 32-byte store
         const bool vec = a.N % PER == 0 && (uintptr_t)a.y % 32 == 0;
-        int it = 0;
+        Slot d;
         for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
             const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
             const int rl = rank * 128 + 32 * q + lane;  // row inside the tile
@@ -522,29 +566,31 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
 #pragma unroll
             for (int i = 0; i < HALF / 2; ++i) acc[i] = 0ull;
             float x_next = xsc[0], w_next = wsc[0];
-            for (int kb = 0; kb < a.kb; ++kb, ++it) {
-                const int d = it % W::kBufs;
+            for (int kb = 0; kb < a.kb; ++kb) {
                 const float sc = x_next * w_next;
                 const uint64_t s2 = ((uint64_t)__float_as_uint(sc) << 32) | __float_as_uint(sc);
                 if (kb + 1 < a.kb) x_next = xsc[kb + 1], w_next = wsc[kb + 1];
-                timed_out = !mbar_wait(dfull + d, (uint32_t)((it / W::kBufs) & 1));
+                timed_out = !mbar_wait(dfull + d.i, d.round);
                 if (timed_out) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32) {
                     uint32_t v0[16], v1[16];
-                    tmem_ld16(lane_base + (uint32_t)(d * BN + c), v0);
-                    tmem_ld16(lane_base + (uint32_t)(d * BN + c + 16), v1);
+                    tmem_ld16(lane_base + (uint32_t)(d.i * BN + c), v0);
+                    tmem_ld16(lane_base + (uint32_t)(d.i * BN + c + 16), v1);
                     tmem_wait_ld();
+                    if (c + 32 == HALF) {  // all read: the buffer is free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_peer(map_rank(smem_u32(dempty + d.i), 0));
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         fma2_acc(acc[c / 2 + i], s2, v0[2 * i], v0[2 * i + 1]);
                         fma2_acc(acc[c / 2 + 8 + i], s2, v1[2 * i], v1[2 * i + 1]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_peer(map_rank(smem_u32(dempty + d), 0));
+                d.next(W::kBufs);
             }
             if (!live || timed_out) continue;
             auto value = [&](int c) {
@@ -615,7 +661,7 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : (tiles < sms ? tiles : sms)));
-    cfg.blockDim = dim3(kStreamThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at;
