@@ -48,24 +48,45 @@ Q4_DEVINL void unpack16(const uint4 &r, float *v) {
     }
 }
 
-// N consecutive values from p, `left` of them inside the row (zeros behind).
+// N consecutive values of a row, of which `left` (which may be negative) are inside it; zeros
+// behind. The loads and their conversion are apart, so that a thread has all of its loads on
+// their way before it waits for the first.
 template <typename T, int N, bool VEC>
-Q4_DEVINL void load_values(const T *p, int64_t left, float (&v)[N]) {
-    if constexpr (VEC) {
-        constexpr int PER = 16 / sizeof(T);
-        if (left > 0) {  // rows are whole 16-byte units here
+struct Chunk {
+    static constexpr int PER = 16 / (int)sizeof(T);
+    typename std::conditional<VEC, uint4, T>::type raw[VEC ? N / PER : N];
+    Q4_DEVINL void load(const T *p, int left) {
+        if constexpr (VEC) {  // rows are whole 16-byte units here
 #pragma unroll
-            for (int i = 0; i < N / PER; ++i) unpack16<T>(reinterpret_cast<const uint4 *>(p)[i], v + i * PER);
+            for (int i = 0; i < N / PER; ++i) {
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (left > 0) raw[i] = reinterpret_cast<const uint4 *>(p)[i];
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.f;
+            for (int i = 0; i < N; ++i) {
+                raw[i] = T(0.f);
+                if (i < left) raw[i] = p[i];
+            }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
     }
-}
+    Q4_DEVINL void values(float (&v)[N]) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < N / PER; ++i) unpack16<T>(raw[i], v + i * PER);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = to_f32(raw[i]);
+        }
+    }
+};
 
+// max(m, |v|), NaN if either is: a block's NaN or Inf stays visible in its maximum.
+Q4_DEVINL float abs_max(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
 Q4_DEVINL uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 Q4_DEVINL float block_scale(uint32_t maxbits) {
@@ -104,10 +125,18 @@ Q4_DEVINL uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// silu(g) u = g u / (1 + exp(-g)), in fp32 with the hardware's exponential and reciprocal
-// (relative error at most (10 + 1.2 |g|) 2^-23; the code that follows keeps 4 bits). For
-// gates below about -88 the exponential is infinite and the value 0.
-Q4_DEVINL float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+// silu(g) u = g u / (1 + 2^(-g log2 e)), in fp32 with the hardware's exponential and
+// reciprocal, results below 2^-126 taken as 0 (the plain forms' steps for such results made
+// the kernel compute-bound). Error: t = -g log2 e is off by at most |t| 2^-23 in all (its
+// rounding and the constant's), so 2^t by |g| 2^-23 relative, to which the exponential, the
+// sum, the reciprocal and the two products add at most 8 x 2^-23; the code that follows
+// keeps 4 bits. For gates below about -88 the sum is infinite and the value 0.
+Q4_DEVINL float silu_mul(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return g * r * u;
+}
 
 struct RowsArgs {
     const void *x;
@@ -125,35 +154,54 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
     const int sub = threadIdx.x & 15;
     const uint32_t first = blockIdx.x * (16 * U) + (threadIdx.x >> 4);
     const int64_t live = a.count ? (int64_t)*a.count : INT64_MAX;
-    float v[U][8];
-    int64_t left[U];
+    Chunk<T, 8, VEC> x[U], up[SILU ? U : 1];
+    int left[U];
     uint32_t row[U], blk[U];
     bool on[U];
+    row[0] = first / a.kb;
+    blk[0] = first - row[0] * a.kb;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        const uint32_t u = first + 16 * j;
-        on[j] = u < a.units;
-        row[j] = on[j] ? u / a.kb : 0;
-        blk[j] = on[j] ? u - row[j] * a.kb : 0;
-        int64_t src = row[j];
-        if (on[j] && a.rows) src = a.rows[row[j]];
-        on[j] = on[j] && src >= 0 && src < a.x_rows && (int64_t)row[j] < live;
-        const int64_t k0 = (int64_t)blk[j] * 128 + 8 * sub;
-        left[j] = on[j] ? a.K - k0 : 0;
-        const T *p = static_cast<const T *>(a.x) + (on[j] ? src * a.ldx + k0 : 0);
-        load_values<T, 8, VEC>(p, left[j], v[j]);
-        if constexpr (SILU) {
-            float up[8];
-            load_values<T, 8, VEC>(p + a.K, left[j], up);
+        if (j > 0) {  // 16 blocks on, over as many rows as that is
+            row[j] = row[j - 1];
+            blk[j] = blk[j - 1] + 16;
+            if (blk[j] >= a.kb) {
+                row[j] += blk[j] / a.kb;
+                blk[j] %= a.kb;
+            }
+        }
+        on[j] = first + 16 * j < a.units && (int64_t)row[j] < live;
+        left[j] = on[j] ? (int)a.K - (int)blk[j] * 128 - 8 * sub : 0;
+    }
+    int64_t src[U];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = silu_mul(v[j][i], up[i]);
+    for (int j = 0; j < U; ++j) {
+        src[j] = row[j];
+        if (a.rows && on[j]) {
+            src[j] = a.rows[row[j]];
+            if (src[j] < 0 || src[j] >= a.x_rows) on[j] = false, left[j] = 0, src[j] = 0;
         }
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        uint32_t m = 0;
+        const T *p = static_cast<const T *>(a.x) + src[j] * a.ldx + (int64_t)blk[j] * 128 + 8 * sub;
+        x[j].load(p, left[j]);
+        if constexpr (SILU) up[j].load(p + a.K, left[j]);
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[j][i]));
+    for (int j = 0; j < U; ++j) {
+        float v[8];
+        x[j].values(v);
+        if constexpr (SILU) {
+            float u[8];
+            up[j].values(u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = abs_max(big, v[i]);
+        uint32_t m = abs_bits(big);
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (!on[j]) continue;
@@ -161,7 +209,7 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
         const BlockDiv d = make_block_div(s);
         float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = quotient(d, v[j][i]);
+        for (int i = 0; i < 8; ++i) q[i] = quotient(d, v[i]);
         const uint32_t lo = e4m3x4(q[0], q[1], q[2], q[3]), hi = e4m3x4(q[4], q[5], q[6], q[7]);
         uint8_t *c = a.codes + (int64_t)row[j] * a.K + (int64_t)blk[j] * 128 + 8 * sub;
         if constexpr (VEC) {
@@ -179,34 +227,40 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
 }
 
 // One 128 x 128 block of [.., N, K] weights a CTA. PER values a lane and load; a row's 128
-// columns are 128 / PER lanes wide, so 256 threads pass over the block in 64 / PER steps.
+// columns are 128 / PER lanes wide, so 512 threads pass over the block in 32 / PER steps and
+// keep 32 values each: two CTAs an SM then have 128 KB of fp32 on their way (with 256 threads
+// of 64 values one CTA filled the registers and nothing covered its loads).
+constexpr int kTileThreads = 512;
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) fp8_pack_tiles(const T *__restrict__ w, int64_t N, int64_t K, uint32_t nb,
+__global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__restrict__ w, int64_t N, int64_t K, uint32_t nb,
                                                       uint32_t kb, uint8_t *__restrict__ codes,
                                                       float *__restrict__ scales, uint32_t *status) {
-    constexpr int PER = 16 / sizeof(T), LANES = 128 / PER, ROWS = 256 / LANES, STEPS = 128 / ROWS;
+    constexpr int PER = 16 / sizeof(T), LANES = 128 / PER, ROWS = kTileThreads / LANES, STEPS = 128 / ROWS;
     const uint32_t t = blockIdx.x / kb, kblk = blockIdx.x - t * kb;  // t: (matrix, row block)
     const uint32_t e = t / nb, nblk = t - e * nb;
     const int64_t k0 = (int64_t)kblk * 128 + (threadIdx.x % LANES) * PER;
     const int64_t n0 = (int64_t)nblk * 128 + threadIdx.x / LANES;
     const T *src = w + (int64_t)e * N * K;
-    float v[STEPS][PER];
-    uint32_t m = 0;
+    Chunk<T, PER, VEC> raw[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const int64_t n = n0 + i * ROWS;
-        load_values<T, PER, VEC>(src + (n < N ? n * K + k0 : 0), n < N ? K - k0 : 0, v[i]);
+        raw[i].load(src + (n < N ? n * K + k0 : 0), n < N ? (int)(K - k0) : 0);
     }
+    float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i)
+    for (int i = 0; i < STEPS; ++i) {
+        float v[PER];
+        raw[i].values(v);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) m = max(m, abs_bits(v[i][j]));
-    m = __reduce_max_sync(0xffffffffu, m);
-    __shared__ uint32_t part[8];
+        for (int j = 0; j < PER; ++j) big = abs_max(big, v[j]);
+    }
+    uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(big));
+    __shared__ uint32_t part[kTileThreads / 32];
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+    for (int i = 0; i < kTileThreads / 32; ++i) m = max(m, part[i]);
     const float s = block_scale(m);
     const BlockDiv d = make_block_div(s);
     uint8_t *dst = codes + (int64_t)e * N * K;
@@ -214,11 +268,13 @@ __global__ void __launch_bounds__(256) fp8_pack_tiles(const T *__restrict__ w, i
     for (int i = 0; i < STEPS; ++i) {
         const int64_t n = n0 + i * ROWS;
         if (n >= N) continue;
+        float v[PER];
+        raw[i].values(v);
         uint32_t c[PER / 4];
 #pragma unroll
         for (int j = 0; j < PER / 4; ++j)
-            c[j] = e4m3x4(quotient(d, v[i][4 * j]), quotient(d, v[i][4 * j + 1]), quotient(d, v[i][4 * j + 2]),
-                          quotient(d, v[i][4 * j + 3]));
+            c[j] = e4m3x4(quotient(d, v[4 * j]), quotient(d, v[4 * j + 1]), quotient(d, v[4 * j + 2]),
+                          quotient(d, v[4 * j + 3]));
         uint8_t *p = dst + n * K + k0;
         if constexpr (VEC) {
             if (k0 < K) {
@@ -267,9 +323,9 @@ cudaError_t pack_tiles(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *
     const uint32_t nb = (uint32_t)((N + 127) / 128), kb = (uint32_t)((K + 127) / 128);
     const unsigned grid = (unsigned)(E * nb * kb);
     if (vec)
-        fp8_pack_tiles<T, true><<<grid, 256, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
+        fp8_pack_tiles<T, true><<<grid, kTileThreads, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
     else
-        fp8_pack_tiles<T, false><<<grid, 256, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
+        fp8_pack_tiles<T, false><<<grid, kTileThreads, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
     return cudaGetLastError();
 }
 
