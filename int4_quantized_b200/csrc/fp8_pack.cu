@@ -6,8 +6,8 @@
 // is 128 consecutive values of a row (activations), or 128 rows x 128 columns (weights);
 // blocks at the right and lower edges hold what is left.
 //
-//   fp8_pack_rows   16 lanes take one block, 8 values each: one pass over x, the block's
-//                   maximum by four shuffles, one 8-byte store of codes a lane. Source rows
+//   fp8_pack_rows   8 lanes take one block, 16 values each: one pass over x, the block's
+//                   maximum by three shuffles, one 16-byte store of codes a lane. Source rows
 //                   may be given by index (tokens sorted by expert on the way), and the
 //                   values may be silu(gate) * up of rows that hold gate and up side by side.
 //   fp8_pack_tiles  one CTA takes one 128 x 128 block, which stays in registers between the
@@ -29,10 +29,11 @@ Q4_DEVINL float to_f32(float v) { return v; }
 Q4_DEVINL float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 Q4_DEVINL float to_f32(__half v) { return __half2float(v); }
 
-// 16 bytes of T as fp32 values.
-template <typename T>
+// 16 bytes of T as fp32 values (NEG: negated).
+template <typename T, bool NEG>
 Q4_DEVINL void unpack16(const uint4 &r, float *v) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    constexpr uint32_t sign = !NEG ? 0u : sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
+    const uint32_t w[4] = {r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(T) == 4) {
@@ -48,19 +49,31 @@ Q4_DEVINL void unpack16(const uint4 &r, float *v) {
     }
 }
 
+// 32 bytes (a whole sector) in one load.
+Q4_DEVINL void ld_v8(const void *p, uint4 &a, uint4 &b) {
+    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+        : "l"(p));
+}
+
 // N consecutive values of a row, of which `left` (which may be negative) are inside it; zeros
 // behind. The loads and their conversion are apart, so that a thread has all of its loads on
-// their way before it waits for the first.
+// their way before it waits for the first. NEG gives the values negated.
 template <typename T, int N, bool VEC>
 struct Chunk {
     static constexpr int PER = 16 / (int)sizeof(T);
     typename std::conditional<VEC, uint4, T>::type raw[VEC ? N / PER : N];
     Q4_DEVINL void load(const T *p, int left) {
-        if constexpr (VEC) {  // rows are whole 16-byte units here
+        if constexpr (VEC) {  // a row's values are whole chunks of N here
 #pragma unroll
-            for (int i = 0; i < N / PER; ++i) {
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (left > 0) raw[i] = reinterpret_cast<const uint4 *>(p)[i];
+            for (int i = 0; i < N / PER; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+            if (left > 0) {
+                if constexpr (N / PER == 1) {
+                    raw[0] = *reinterpret_cast<const uint4 *>(p);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N / PER; i += 2) ld_v8(p + i * PER, raw[i], raw[i + 1]);
+                }
             }
         } else {
 #pragma unroll
@@ -70,53 +83,80 @@ struct Chunk {
             }
         }
     }
+    template <bool NEG>
     Q4_DEVINL void values(float (&v)[N]) const {
         if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < N / PER; ++i) unpack16<T>(raw[i], v + i * PER);
+            for (int i = 0; i < N / PER; ++i) unpack16<T, NEG>(raw[i], v + i * PER);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = to_f32(raw[i]);
+            for (int i = 0; i < N; ++i) v[i] = NEG ? -to_f32(raw[i]) : to_f32(raw[i]);
         }
     }
 };
 
-// max(m, |v|), NaN if either is: a block's NaN or Inf stays visible in its maximum.
-Q4_DEVINL float abs_max(float m, float v) {
+// max(m, |a|, |b|) for m >= 0, NaN if any is: a block's NaN or Inf stays visible in its maximum.
+Q4_DEVINL float abs_max(float m, float a, float b) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
     return r;
 }
 Q4_DEVINL uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-Q4_DEVINL float block_scale(uint32_t maxbits) {
-    const float s = __fdiv_rn(__uint_as_float(maxbits), kE4m3Max);
-    return s == 0.f ? 1.f : s;
+// Two fp32 values in one 64-bit register, and arithmetic on both in one instruction.
+Q4_DEVINL uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+Q4_DEVINL float2 halves(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+Q4_DEVINL uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+Q4_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // fl32(v / s) by the reciprocal and two residual corrections (P. Markstein, "IA-64 and
 // Elementary Functions", 2000: with y = RN(1/s) and a quotient within one ulp, one more
-// RN(q + RN-exact(v - q s) y) is the correctly rounded quotient; the first correction
-// brings RN(v y), up to two ulps off, within one). The residuals are exact while they stay
-// above the subnormal range: s >= 2^-90, and quotients below 2^-11, where they might not,
-// give the code 0 in any case. Other scales take the division itself. The residuals are
-// formed as q s - v so that v = -0 keeps its sign.
-struct BlockDiv {
-    float s, r;
-    bool fast;
-};
-Q4_DEVINL BlockDiv make_block_div(float s) {
-    BlockDiv d;
-    d.s = s;
-    d.fast = s >= 0x1p-90f && s <= 0x1p120f;
-    d.r = d.fast ? __frcp_rn(s) : 0.f;
-    return d;
+// correction by the exact residual gives the correctly rounded quotient; the first
+// correction brings RN(v y), up to two ulps off, within one). The residuals are exact while
+// they stay above the subnormal range: s >= 2^-90, and quotients below 2^-11, where they
+// might not, give the code 0 in any case. Other scales take the division itself.
+// The values come negated (nv = -v, nr = -1/s): q = nv nr, and the residual q s - v is then
+// one fma, and v = -0 keeps its sign.
+Q4_DEVINL uint64_t quotients(uint64_t nv, uint64_t s, uint64_t nr) {
+    const uint64_t q0 = mul2(nv, nr);
+    const uint64_t q1 = fma2(fma2(q0, s, nv), nr, q0);
+    return fma2(fma2(q1, s, nv), nr, q1);
 }
-Q4_DEVINL float quotient(const BlockDiv &d, float v) {
-    if (!d.fast) return __fdiv_rn(v, d.s);
-    const float q0 = __fmul_rn(v, d.r);
-    const float q1 = __fmaf_rn(-__fmaf_rn(q0, d.s, -v), d.r, q0);
-    return __fmaf_rn(-__fmaf_rn(q1, d.s, -v), d.r, q1);
+
+struct BlockDiv {
+    float s, nr;  // the scale; -1/s, or 0 where the division itself is taken
+};
+// The scale of a block whose largest magnitude is a: fl32(a / 448), by the same corrections
+// with 1/448 where they are exact; 0 becomes 1.
+Q4_DEVINL BlockDiv block_div(float a) {
+    BlockDiv d;
+    if (a >= 0x1p-80f && a < 0x1p127f) {
+        constexpr float y = 1.f / kE4m3Max;  // rounded to nearest by the compiler
+        const float q0 = a * y;
+        const float q1 = __fmaf_rn(-__fmaf_rn(q0, kE4m3Max, -a), y, q0);
+        d.s = __fmaf_rn(-__fmaf_rn(q1, kE4m3Max, -a), y, q1);
+    } else {
+        d.s = __fdiv_rn(a, kE4m3Max);
+        if (d.s == 0.f) d.s = 1.f;
+    }
+    d.nr = d.s >= 0x1p-90f && d.s <= 0x1p120f ? -__frcp_rn(d.s) : 0.f;
+    return d;
 }
 Q4_DEVINL uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
@@ -125,16 +165,36 @@ Q4_DEVINL uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// The codes of N values given negated.
+template <int N>
+Q4_DEVINL void codes_of(const float (&nv)[N], const BlockDiv &d, uint32_t (&c)[N / 4]) {
+    float q[N];
+    if (d.nr != 0.f) {
+        const uint64_t s = pair(d.s, d.s), nr = pair(d.nr, d.nr);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 f = halves(quotients(pair(nv[i], nv[i + 1]), s, nr));
+            q[i] = f.x, q[i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i] = __fdiv_rn(-nv[i], d.s);
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) c[i] = e4m3x4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+}
+
 // silu(g) u = g u / (1 + 2^(-g log2 e)), in fp32 with the hardware's exponential and
 // reciprocal, results below 2^-126 taken as 0 (the plain forms' steps for such results made
 // the kernel compute-bound). Error: t = -g log2 e is off by at most |t| 2^-23 in all (its
 // rounding and the constant's), so 2^t by |g| 2^-23 relative, to which the exponential, the
 // sum, the reciprocal and the two products add at most 8 x 2^-23; the code that follows
-// keeps 4 bits. For gates below about -88 the sum is infinite and the value 0.
-Q4_DEVINL float silu_mul(float g, float u) {
+// keeps 4 bits. For gates below about -88 the sum is infinite and the value 0. Returned
+// negated, as the quotients want it.
+Q4_DEVINL float neg_silu_mul(float g, float u) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(-1.f - e));
     return g * r * u;
 }
 
@@ -151,10 +211,10 @@ struct RowsArgs {
 
 template <typename T, bool SILU, bool VEC, int U>
 __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
-    const int sub = threadIdx.x & 15;
-    const uint32_t first = blockIdx.x * (16 * U) + (threadIdx.x >> 4);
-    const int64_t live = a.count ? (int64_t)*a.count : INT64_MAX;
-    Chunk<T, 8, VEC> x[U], up[SILU ? U : 1];
+    const int sub = threadIdx.x & 7;
+    const uint32_t first = blockIdx.x * (32 * U) + (threadIdx.x >> 3);
+    const uint32_t live = a.count ? (uint32_t)max(*a.count, 0) : UINT32_MAX;
+    Chunk<T, 16, VEC> x[U], up[SILU ? U : 1];
     int left[U];
     uint32_t row[U], blk[U];
     bool on[U];
@@ -162,16 +222,16 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
     blk[0] = first - row[0] * a.kb;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        if (j > 0) {  // 16 blocks on, over as many rows as that is
+        if (j > 0) {  // 32 blocks on, over as many rows as that is
             row[j] = row[j - 1];
-            blk[j] = blk[j - 1] + 16;
+            blk[j] = blk[j - 1] + 32;
             if (blk[j] >= a.kb) {
                 row[j] += blk[j] / a.kb;
                 blk[j] %= a.kb;
             }
         }
-        on[j] = first + 16 * j < a.units && (int64_t)row[j] < live;
-        left[j] = on[j] ? (int)a.K - (int)blk[j] * 128 - 8 * sub : 0;
+        on[j] = first + 32 * j < a.units && row[j] < live;
+        left[j] = on[j] ? (int)a.K - (int)blk[j] * 128 - 16 * sub : 0;
     }
     int64_t src[U];
 #pragma unroll
@@ -184,44 +244,58 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        const T *p = static_cast<const T *>(a.x) + src[j] * a.ldx + (int64_t)blk[j] * 128 + 8 * sub;
+        const T *p = static_cast<const T *>(a.x) + src[j] * a.ldx + (blk[j] * 128 + 16 * sub);
         x[j].load(p, left[j]);
         if constexpr (SILU) up[j].load(p + a.K, left[j]);
     }
+    float nv[U][16];
+    uint32_t m[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        float v[8];
-        x[j].values(v);
         if constexpr (SILU) {
-            float u[8];
-            up[j].values(u);
+            float g[16], u[16];
+            x[j].template values<false>(g);
+            up[j].template values<false>(u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
+            for (int i = 0; i < 16; ++i) nv[j][i] = neg_silu_mul(g[i], u[i]);
+        } else {
+            x[j].template values<true>(nv[j]);
         }
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) big = abs_max(big, v[i]);
-        uint32_t m = abs_bits(big);
+        for (int i = 0; i < 16; i += 2) big = abs_max(big, nv[j][i], nv[j][i + 1]);
+        m[j] = abs_bits(big);
+    }
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int o = 4; o; o >>= 1) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+    // the scale and its reciprocal cost about as much as a lane's sixteen quotients: lane j of
+    // the eight works them out for block j
+    uint32_t mine = m[0];
+#pragma unroll
+    for (int j = 1; j < U; ++j)
+        if (sub == j) mine = m[j];
+    const BlockDiv own = block_div(__uint_as_float(mine));
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        BlockDiv d;
+        d.s = __shfl_sync(0xffffffffu, own.s, j, 8);
+        d.nr = __shfl_sync(0xffffffffu, own.nr, j, 8);
         if (!on[j]) continue;
-        const float s = block_scale(m);
-        const BlockDiv d = make_block_div(s);
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = quotient(d, v[i]);
-        const uint32_t lo = e4m3x4(q[0], q[1], q[2], q[3]), hi = e4m3x4(q[4], q[5], q[6], q[7]);
-        uint8_t *c = a.codes + (int64_t)row[j] * a.K + (int64_t)blk[j] * 128 + 8 * sub;
+        uint32_t c[4];
+        codes_of<16>(nv[j], d, c);
+        uint8_t *p = a.codes + (int64_t)row[j] * a.K + (blk[j] * 128 + 16 * sub);
         if constexpr (VEC) {
-            if (left[j] > 0) *reinterpret_cast<uint2 *>(c) = make_uint2(lo, hi);
+            if (left[j] > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left[j]) c[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+            for (int i = 0; i < 16; ++i)
+                if (i < left[j]) p[i] = (uint8_t)(c[i / 4] >> (8 * (i & 3)));
         }
-        if (sub == 0) {
-            a.scales[(int64_t)row[j] * a.kb + blk[j]] = s;
-            if (m >= kInf && a.status) atomicOr(a.status, Q4_STATUS_NONFINITE);
+        if (sub == j) {
+            a.scales[(int64_t)row[j] * a.kb + blk[j]] = d.s;
+            if (m[j] >= kInf && a.status) atomicOr(a.status, Q4_STATUS_NONFINITE);
         }
     }
 }
@@ -251,9 +325,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__res
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         float v[PER];
-        raw[i].values(v);
+        raw[i].template values<false>(v);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) big = abs_max(big, v[j]);
+        for (int j = 0; j < PER; j += 2) big = abs_max(big, v[j], v[j + 1]);
     }
     uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(big));
     __shared__ uint32_t part[kTileThreads / 32];
@@ -261,20 +335,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__res
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kTileThreads / 32; ++i) m = max(m, part[i]);
-    const float s = block_scale(m);
-    const BlockDiv d = make_block_div(s);
+    const BlockDiv d = block_div(__uint_as_float(m));
     uint8_t *dst = codes + (int64_t)e * N * K;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const int64_t n = n0 + i * ROWS;
         if (n >= N) continue;
-        float v[PER];
-        raw[i].values(v);
+        float nv[PER];
+        raw[i].template values<true>(nv);
         uint32_t c[PER / 4];
-#pragma unroll
-        for (int j = 0; j < PER / 4; ++j)
-            c[j] = e4m3x4(quotient(d, v[4 * j]), quotient(d, v[4 * j + 1]), quotient(d, v[4 * j + 2]),
-                          quotient(d, v[4 * j + 3]));
+        codes_of<PER>(nv, d, c);
         uint8_t *p = dst + n * K + k0;
         if constexpr (VEC) {
             if (k0 < K) {
@@ -290,27 +360,26 @@ __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__res
         }
     }
     if (threadIdx.x == 0) {
-        scales[blockIdx.x] = s;
+        scales[blockIdx.x] = d.s;
         if (m >= kInf && status) atomicOr(status, Q4_STATUS_NONFINITE);
     }
 }
 
 template <typename T>
 cudaError_t pack_rows(const RowsArgs &a, bool silu, cudaStream_t st) {
-    // whole 16-byte units a row: aligned loads of x and 8-byte stores of codes
-    const bool vec = a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.codes % 8 == 0 &&
-                     (a.ldx * (int64_t)sizeof(T)) % 16 == 0;
-    // four blocks a half warp keep the loads in flight that HBM needs; with fewer blocks than
-    // fill the machine so, one each (16 x 4096: 32 CTAs instead of 8)
-    const bool four = a.units >= 148 * 16 * 4;
-    const unsigned grid = (a.units + (four ? 63 : 15)) / (four ? 64 : 16);
+    // whole chunks of 16 values a row: 32-byte loads of x and 16-byte stores of codes
+    const bool vec = a.K % 16 == 0 && (uintptr_t)a.x % 32 == 0 && (uintptr_t)a.codes % 16 == 0;
+    // two blocks a group of lanes keep the loads in flight that HBM needs; with fewer blocks
+    // than fill the machine so, one each (16 x 4096: 16 CTAs instead of 8)
+    const bool two = a.units >= 148 * 32 * 2 * 2;
+    const unsigned grid = (a.units + (two ? 63 : 31)) / (two ? 64 : 32);
 #define Q4_ROWS(S, V, U) fp8_pack_rows<T, S, V, U><<<grid, 256, 0, st>>>(a)
     if (silu) {
-        if (vec) four ? Q4_ROWS(true, true, 4) : Q4_ROWS(true, true, 1);
-        else four ? Q4_ROWS(true, false, 4) : Q4_ROWS(true, false, 1);
+        if (vec) two ? Q4_ROWS(true, true, 2) : Q4_ROWS(true, true, 1);
+        else two ? Q4_ROWS(true, false, 2) : Q4_ROWS(true, false, 1);
     } else {
-        if (vec) four ? Q4_ROWS(false, true, 4) : Q4_ROWS(false, true, 1);
-        else four ? Q4_ROWS(false, false, 4) : Q4_ROWS(false, false, 1);
+        if (vec) two ? Q4_ROWS(false, true, 2) : Q4_ROWS(false, true, 1);
+        else two ? Q4_ROWS(false, false, 2) : Q4_ROWS(false, false, 1);
     }
 #undef Q4_ROWS
     return cudaGetLastError();
