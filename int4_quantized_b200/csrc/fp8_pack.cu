@@ -300,16 +300,16 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
     }
 }
 
-// One 128 x 128 block of [.., N, K] weights a CTA. PER values a lane and load; a row's 128
-// columns are 128 / PER lanes wide, so 512 threads pass over the block in 32 / PER steps and
-// keep 32 values each: two CTAs an SM then have 128 KB of fp32 on their way (with 256 threads
+// One 128 x 128 block of [.., N, K] weights a CTA. PER values (32 bytes) a lane and load; a
+// row's 128 columns are 128 / PER lanes wide, so 512 threads pass over the block in 32 / PER
+// steps and keep 32 values each: two CTAs an SM then have 128 KB of fp32 on their way (with 256 threads
 // of 64 values one CTA filled the registers and nothing covered its loads).
 constexpr int kTileThreads = 512;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__restrict__ w, int64_t N, int64_t K, uint32_t nb,
                                                       uint32_t kb, uint8_t *__restrict__ codes,
                                                       float *__restrict__ scales, uint32_t *status) {
-    constexpr int PER = 16 / sizeof(T), LANES = 128 / PER, ROWS = kTileThreads / LANES, STEPS = 128 / ROWS;
+    constexpr int PER = 32 / sizeof(T), LANES = 128 / PER, ROWS = kTileThreads / LANES, STEPS = 128 / ROWS;
     const uint32_t t = blockIdx.x / kb, kblk = blockIdx.x - t * kb;  // t: (matrix, row block)
     const uint32_t e = t / nb, nblk = t - e * nb;
     const int64_t k0 = (int64_t)kblk * 128 + (threadIdx.x % LANES) * PER;
@@ -348,10 +348,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__res
         uint8_t *p = dst + n * K + k0;
         if constexpr (VEC) {
             if (k0 < K) {
-                if constexpr (PER == 8)
-                    *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
+                if constexpr (PER == 16)
+                    *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
                 else
-                    *reinterpret_cast<uint32_t *>(p) = c[0];
+                    *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
             }
         } else {
 #pragma unroll
@@ -388,7 +388,7 @@ cudaError_t pack_rows(const RowsArgs &a, bool silu, cudaStream_t st) {
 template <typename T>
 cudaError_t pack_tiles(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *codes, float *scales, uint32_t *status,
                        cudaStream_t st) {
-    const bool vec = (K * (int64_t)sizeof(T)) % 16 == 0 && (uintptr_t)w % 16 == 0 && (uintptr_t)codes % 8 == 0;
+    const bool vec = (K * (int64_t)sizeof(T)) % 32 == 0 && (uintptr_t)w % 32 == 0 && (uintptr_t)codes % 16 == 0;
     const uint32_t nb = (uint32_t)((N + 127) / 128), kb = (uint32_t)((K + 127) / 128);
     const unsigned grid = (unsigned)(E * nb * kb);
     if (vec)
