@@ -7,17 +7,18 @@
 // no call writes their rows.
 //
 //   moe_sort_kernel   one cluster of up to 8 CTAs: every warp counts a run of slots into a
-//                     histogram of its own (__match_any groups equal ids, so one lane adds
-//                     for all of them), the CTAs read each other's totals through
+//                     histogram of its own, the CTAs read each other's totals through
 //                     distributed shared memory, and the warps walk their runs again and
-//                     hand out the places in slot order. One launch, no workspace, no
-//                     atomics: the result is the stable order, the same on every run.
-//   moe_gather_kernel one warp copies up to 4 KB of a row.
+//                     hand out the places in slot order (a lane's rank among equal ids of its
+//                     32 slots comes from one vote a bit). One launch, no workspace, and only
+//                     counts are added atomically: the result is the stable order on every run.
+//   moe_gather_kernel one warp copies up to 4 KB: part of a row, or several short rows.
 //   moe_combine_kernel out[t] = sum over j of w[t, j] ys[pos[t, j]], in fp32, j ascending,
 //                     rounded once; without weights it is the gradient of the gather.
-//   moe_combine_bwd   one CTA a token: reads dout[t] once for all its slots, writes
-//                     dys[pos] = w dout and dw = <dout, ys[pos]>.
-// All but the sort are bound by the rows they read and write.
+//   moe_combine_bwd   four warps or one for each token: dout[t] is read once for all its
+//                     slots, dys[pos] = w dout is written and dw = <dout, ys[pos]> summed.
+// All but the sort are bound by the rows they read and write; each lane has up to 8 accesses
+// of 16 bytes on their way.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -31,109 +32,144 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortWarps = 32;  // at most, in one CTA
 constexpr int kSortCtas = 8;
+constexpr int kSortBatch = 8;   // chunks of 32 ids a warp has on their way
 constexpr int64_t kMaxExperts = 1024;  // 32 warps x 1024 counters of 4 bytes: 128 KB of shared memory
 
+// The expert of each lane's slot in kSortBatch chunks from s on; -1 behind end and for ids
+// outside 0 .. E - 1.
 template <typename T>
-Q4_DEVINL int expert_of(const T *ids, int64_t s, int64_t end, int E) {
-    if (s >= end) return -1;
-    const T e = ids[s];
-    return e >= 0 && e < (T)E ? (int)e : -1;
+Q4_DEVINL void load_ids(const T *ids, int64_t s, int64_t end, int E, int (&e)[kSortBatch]) {
+    T raw[kSortBatch];
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i) {
+        const int64_t at = s + 32 * i + (threadIdx.x & 31);
+        raw[i] = (T)-1;
+        if (at < end) raw[i] = ids[at];
+    }
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i) e[i] = raw[i] >= 0 && raw[i] < (T)E ? (int)raw[i] : -1;
+}
+
+// The lanes whose e (0 .. 2^bits - 1) equals this lane's, by one vote a bit (__match_any_sync
+// took about 90 cycles a warp and SM: 65536 ids of 256 experts 24 us).
+Q4_DEVINL uint32_t same_lanes(int e, int bits) {
+    uint32_t same = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (e >> b) & 1;
+        const uint32_t v = __ballot_sync(0xffffffffu, one);
+        same &= one ? v : ~v;
+    }
+    return same;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const T *__restrict__ ids, int64_t R, int k, int E,
-                                                                int32_t *__restrict__ tokens,
-                                                                int32_t *__restrict__ pos,
-                                                                int32_t *__restrict__ offsets) {
+__global__ void __launch_bounds__(32 * kSortWarps) moe_sort_kernel(const T *__restrict__ ids, int64_t R, int k, int E,
+                                                                   int32_t *__restrict__ tokens,
+                                                                   int32_t *__restrict__ pos,
+                                                                   int32_t *__restrict__ offsets) {
     extern __shared__ int32_t sm[];
-    int32_t *hist = sm;                      // [warps][E]: counts, then the next place of each (warp, expert)
-    int32_t *tot = sm + kSortWarps * E;      // [E] this CTA's counts, read by the others
-    int32_t *start = tot + E;                // [E + 1] the experts' first places
+    const int W = blockDim.x >> 5;
+    int32_t *hist = sm;            // [W][E]: counts, then each warp's next place after the warps before it
+    int32_t *tot = sm + W * E;     // [E] this CTA's counts, read by the others
+    int32_t *base = tot + E;       // [E] the first place of this CTA's slots of each expert
+    int32_t *all = base + E;       // [E + 1] counts, then the experts' first places
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t below = (1u << lane) - 1;
     // runs of whole 32-slot chunks, one a warp
-    const int64_t run = ((R + (int64_t)C * kSortWarps * 32 - 1) / ((int64_t)C * kSortWarps * 32)) * 32;
-    const int64_t s0 = min(R, (int64_t)(c * kSortWarps + warp) * run), s1 = min(R, s0 + run);
+    const int64_t run = ((R + (int64_t)C * W * 32 - 1) / ((int64_t)C * W * 32)) * 32;
+    const int64_t s0 = min(R, (int64_t)(c * W + warp) * run), s1 = min(R, s0 + run);
 
-    for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) hist[i] = 0;
+    int e[kSortBatch];
+    load_ids(ids, s0, s1, E, e);
+    for (int i = threadIdx.x; i < W * E; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     int32_t *mine = hist + warp * E;
-    {
-        int next = expert_of(ids, s0 + lane, s1, E);
-        for (int64_t s = s0; s < s1; s += 32) {
-            const int e = next;
-            next = expert_of(ids, s + 32 + lane, s1, E);
-            const uint32_t same = __match_any_sync(0xffffffffu, e);
-            if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
-            __syncwarp();
+    for (int64_t s = s0; s < s1; s += 32 * kSortBatch) {
+        if (s > s0) load_ids(ids, s, s1, E, e);
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i) {
+            if (e[i] >= 0) atomicAdd(&mine[e[i]], 1);  // a count: its order does not matter
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kSortThreads) {
+    for (int x = threadIdx.x; x < E; x += blockDim.x) {
         int32_t sum = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int32_t n = hist[w * E + e];
-            hist[w * E + e] = sum;
+#pragma unroll 8
+        for (int w = 0; w < W; ++w) {
+            const int32_t n = hist[w * E + x];
+            hist[w * E + x] = sum;
             sum += n;
         }
-        tot[e] = sum;
+        tot[x] = sum;
     }
-    cl.sync();
+    if (C > 1) cl.sync();
+    else __syncthreads();
     // all CTAs' counts of each expert, and those of the CTAs before this one
-    for (int e = threadIdx.x; e < E; e += kSortThreads) {
-        int32_t before = 0, all = 0;
-        for (int r = 0; r < C; ++r) {
-            const int32_t n = cl.map_shared_rank(tot, r)[e];
-            before += r < c ? n : 0;
-            all += n;
+    for (int x = threadIdx.x; x < E; x += blockDim.x) {
+        int32_t before = 0, n = 0;
+        if (C > 1) {
+            int32_t r[kSortCtas];
+#pragma unroll
+            for (int i = 0; i < kSortCtas; ++i) r[i] = i < C ? cl.map_shared_rank(tot, i)[x] : 0;
+#pragma unroll
+            for (int i = 0; i < kSortCtas; ++i) {
+                before += i < c ? r[i] : 0;
+                n += r[i];
+            }
+        } else {
+            n = tot[x];
         }
-        start[e] = all;
-        for (int w = 0; w < kSortWarps; ++w) hist[w * E + e] += before;
+        base[x] = before;
+        all[x] = n;
     }
-    cl.sync();  // no CTA reads another's totals from here on
+    if (C > 1) cl.sync();  // no CTA reads another's totals from here on
+    else __syncthreads();
     if (warp == 0) {  // exclusive sums over the experts
         int32_t carry = 0;
         for (int b = 0; b < E; b += 32) {
-            const int32_t n = b + lane < E ? start[b + lane] : 0;
+            const int32_t n = b + lane < E ? all[b + lane] : 0;
             int32_t x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            __syncwarp();
-            if (b + lane < E) start[b + lane] = carry + x - n;
+            if (b + lane < E) {
+                all[b + lane] = carry + x - n;
+                base[b + lane] += carry + x - n;
+            }
             carry += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (lane == 0) start[E] = carry;
+        if (lane == 0) all[E] = carry;
     }
     __syncthreads();
     if (c == 0)
-        for (int e = threadIdx.x; e <= E; e += kSortThreads) offsets[e] = start[e];
-    {
-        int next = expert_of(ids, s0 + lane, s1, E);
-        for (int64_t s = s0; s < s1; s += 32) {
-            const int e = next;
-            next = expert_of(ids, s + 32 + lane, s1, E);
-            const uint32_t same = __match_any_sync(0xffffffffu, e);
-            const int32_t at = e >= 0 ? mine[e] : 0;
+        for (int x = threadIdx.x; x <= E; x += blockDim.x) offsets[x] = all[x];
+    const int bits = 32 - __clz(E);  // ids 0 .. E - 1, and E for no expert
+    const bool once = run <= 32 * kSortBatch;  // the ids are still in registers
+    for (int64_t s = s0; s < s1; s += 32 * kSortBatch) {
+        if (!once) load_ids(ids, s, s1, E, e);
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i) {
+            const int64_t slot = s + 32 * i + lane;
+            if (s + 32 * i >= s1) break;
+            const uint32_t same = same_lanes(e[i] >= 0 ? e[i] : E, bits);
+            const int32_t at = e[i] >= 0 ? mine[e[i]] : 0;
             __syncwarp();
-            if (e >= 0 && (same & below) == 0) mine[e] = at + __popc(same);
+            if (e[i] >= 0 && (same & below) == 0) mine[e[i]] = at + __popc(same);
             __syncwarp();
-            if (s + lane < s1) {
-                const int32_t p = e >= 0 ? start[e] + at + __popc(same & below) : -1;
-                pos[s + lane] = p;
-                if (e >= 0) tokens[p] = (int32_t)((uint32_t)(s + lane) / (uint32_t)k);
+            if (slot < s1) {
+                const int32_t p = e[i] >= 0 ? base[e[i]] + at + __popc(same & below) : -1;
+                pos[slot] = p;
+                if (e[i] >= 0) tokens[p] = (int32_t)((uint32_t)slot / (uint32_t)k);
             }
         }
     }
-    for (int64_t p = start[E] + (int64_t)c * kSortThreads + threadIdx.x; p < R; p += (int64_t)C * kSortThreads)
-        tokens[p] = -1;
+    for (int64_t p = all[E] + (int64_t)c * blockDim.x + threadIdx.x; p < R; p += (int64_t)C * blockDim.x) tokens[p] = -1;
 }
 
 // ---- rows ---------------------------------------------------------------------------------
@@ -168,32 +204,47 @@ Q4_DEVINL typename Row<T, VEC>::V pack(const float (&f)[Row<T, VEC>::N]) {
     return r;
 }
 
-constexpr int kGatherVecs = 8;  // accesses a lane: 4 KB a warp in 16-byte accesses
+constexpr int kInFlight = 8;  // accesses a lane
 
+// Rows written once: they go first when L2 is full, so that x, which each expert reads again,
+// stays (8192 tokens x 8 of 4096 bf16 values: 132 us without, 122 with).
 template <typename V>
+Q4_DEVINL void store_once(V *p, V v) {
+    __stcs(p, v);
+}
+
+// A warp copies P parts of 32 accesses from each of kInFlight / P rows.
+template <typename V, int P>
 __global__ void __launch_bounds__(256) moe_gather_kernel(const V *__restrict__ x, int64_t T,
                                                          const int32_t *__restrict__ tokens, int64_t R, int64_t per_row,
                                                          uint32_t chunks, V *__restrict__ xs) {
+    constexpr int ROWS = kInFlight / P;
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const uint32_t p = unit / chunks, ch = unit - p * chunks;
-    if (p >= R) return;
-    const int64_t t = tokens[p];
-    if (t < 0 || t >= T) return;
-    const int64_t v0 = (int64_t)ch * (32 * kGatherVecs) + (threadIdx.x & 31);
-    const V *src = x + t * per_row;
-    V *dst = xs + (int64_t)p * per_row;
-    V r[kGatherVecs];
+    const uint32_t g = unit / chunks, ch = unit - g * chunks;
+    const int64_t v0 = (int64_t)ch * (32 * P) + (threadIdx.x & 31);
+    int64_t t[ROWS];
+    V r[ROWS][P];
 #pragma unroll
-    for (int i = 0; i < kGatherVecs; ++i)
-        if (v0 + 32 * i < per_row) r[i] = src[v0 + 32 * i];
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t p = (int64_t)g * ROWS + i;
+        t[i] = p < R ? (int64_t)tokens[p] : -1;
+        if (t[i] >= T) t[i] = -1;
+    }
 #pragma unroll
-    for (int i = 0; i < kGatherVecs; ++i)
-        if (v0 + 32 * i < per_row) dst[v0 + 32 * i] = r[i];
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            if (t[i] >= 0 && v0 + 32 * j < per_row) r[i][j] = x[t[i] * per_row + v0 + 32 * j];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            if (t[i] >= 0 && v0 + 32 * j < per_row)
+                store_once(xs + ((int64_t)g * ROWS + i) * per_row + v0 + 32 * j, r[i][j]);
 }
 
-constexpr int kCombineSlots = 4;  // row loads in flight a lane
-
-template <typename T, bool VEC>
+// A warp sums P parts of 32 accesses of a row, S slots at a time.
+template <typename T, bool VEC, int S, int P>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, VEC>::V *__restrict__ ys, int64_t R,
                                                           const int32_t *__restrict__ pos,
                                                           const float *__restrict__ weights, int64_t tokens, int k,
@@ -204,93 +255,116 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, 
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t t = unit / chunks, ch = unit - t * chunks;
     if (t >= tokens) return;
-    const int64_t v = (int64_t)ch * 32 + (threadIdx.x & 31);
-    if (v >= per_row) return;
+    const int64_t v0 = (int64_t)ch * (32 * P) + (threadIdx.x & 31);
     const int64_t s0 = (int64_t)t * k;
-    float acc[N];
+    float acc[P][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < k; j0 += kCombineSlots) {
-        V r[kCombineSlots];
-        float w[kCombineSlots];
-        bool on[kCombineSlots];
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int j = 0; j < kCombineSlots; ++j) {
+        for (int n = 0; n < N; ++n) acc[i][n] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += S) {
+        V r[S][P];
+        float w[S];
+        bool on[S];
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
             const int32_t p = j0 + j < k ? pos[s0 + j0 + j] : -1;
             on[j] = p >= 0 && p < R;
             w[j] = on[j] && weights ? weights[s0 + j0 + j] : 1.f;
-            if (on[j]) r[j] = ys[(int64_t)p * per_row + v];
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (on[j] && v0 + 32 * i < per_row) r[j][i] = ys[(int64_t)p * per_row + v0 + 32 * i];
         }
 #pragma unroll
-        for (int j = 0; j < kCombineSlots; ++j) {
+        for (int j = 0; j < S; ++j) {
             if (!on[j]) continue;
-            float f[N];
-            unpack<T, VEC>(r[j], f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+            for (int i = 0; i < P; ++i) {
+                float f[N];
+                unpack<T, VEC>(r[j][i], f);
+#pragma unroll
+                for (int n = 0; n < N; ++n) acc[i][n] = fmaf(w[j], f[n], acc[i][n]);
+            }
         }
     }
-    out[(int64_t)t * per_row + v] = pack<T, VEC>(acc);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (v0 + 32 * i < per_row) out[(int64_t)t * per_row + v0 + 32 * i] = pack<T, VEC>(acc[i]);
 }
 
-constexpr int kBwdThreads = 128;
-constexpr int kBwdSlots = 8;  // slots a pass over dout[t]
-
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBwdThreads) moe_combine_bwd(const typename Row<T, VEC>::V *__restrict__ dout,
-                                                               const typename Row<T, VEC>::V *__restrict__ ys,
-                                                               int64_t R, const int32_t *__restrict__ pos,
-                                                               const float *__restrict__ weights, int k,
-                                                               int64_t per_row, typename Row<T, VEC>::V *__restrict__ dys,
-                                                               float *__restrict__ dweights) {
+// W warps take one token, S slots at a time and P accesses of each; 4 / W tokens a CTA.
+template <typename T, bool VEC, int W, int S, int P>
+__global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, VEC>::V *__restrict__ dout,
+                                                       const typename Row<T, VEC>::V *__restrict__ ys, int64_t R,
+                                                       const int32_t *__restrict__ pos,
+                                                       const float *__restrict__ weights, int64_t tokens, int k,
+                                                       int64_t per_row, typename Row<T, VEC>::V *__restrict__ dys,
+                                                       float *__restrict__ dweights) {
     using V = typename Row<T, VEC>::V;
     constexpr int N = Row<T, VEC>::N;
-    __shared__ float part[kBwdThreads / 32][kBwdSlots];
-    const int64_t t = blockIdx.x, s0 = t * k;
-    for (int j0 = 0; j0 < k; j0 += kBwdSlots) {
-        int32_t p[kBwdSlots];
-        float w[kBwdSlots], dot[kBwdSlots];
+    __shared__ float part[4][S];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (4 / W) + warp / W, s0 = t * k;
+    const int at = W > 1 ? (int)threadIdx.x : lane;  // the lane's place among the token's
+    const bool live = t < tokens;  // the same for all of a token's warps
+    for (int j0 = 0; j0 < k; j0 += S) {
+        int32_t p[S];
+        float w[S], dot[S];
 #pragma unroll
-        for (int j = 0; j < kBwdSlots; ++j) {
-            p[j] = j0 + j < k ? pos[s0 + j0 + j] : -1;
+        for (int j = 0; j < S; ++j) {
+            p[j] = live && j0 + j < k ? pos[s0 + j0 + j] : -1;
             if (p[j] >= R) p[j] = -1;
             w[j] = p[j] >= 0 ? weights[s0 + j0 + j] : 0.f;
             dot[j] = 0.f;
         }
-        for (int64_t v = threadIdx.x; v < per_row; v += kBwdThreads) {
-            V r[kBwdSlots];
+        for (int64_t v0 = at; live && v0 < per_row; v0 += 32 * W * P) {
+            V r[S][P], g0[P];
 #pragma unroll
-            for (int j = 0; j < kBwdSlots; ++j)
-                if (p[j] >= 0) r[j] = ys[(int64_t)p[j] * per_row + v];
-            float g[N];
-            unpack<T, VEC>(dout[t * per_row + v], g);
+            for (int i = 0; i < P; ++i) {
+                const int64_t v = v0 + 32 * W * i;
+                if (v < per_row) {
+                    g0[i] = dout[t * per_row + v];
 #pragma unroll
-            for (int j = 0; j < kBwdSlots; ++j) {
-                if (p[j] < 0) continue;
-                float f[N], d[N];
-                unpack<T, VEC>(r[j], f);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    dot[j] = fmaf(g[i], f[i], dot[j]);
-                    d[i] = w[j] * g[i];
+                    for (int j = 0; j < S; ++j)
+                        if (p[j] >= 0) r[j][i] = ys[(int64_t)p[j] * per_row + v];
                 }
-                dys[(int64_t)p[j] * per_row + v] = pack<T, VEC>(d);
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int64_t v = v0 + 32 * W * i;
+                if (v >= per_row) break;
+                float g[N];
+                unpack<T, VEC>(g0[i], g);
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    if (p[j] < 0) continue;
+                    float f[N], d[N];
+                    unpack<T, VEC>(r[j][i], f);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        dot[j] = fmaf(g[n], f[n], dot[j]);
+                        d[n] = w[j] * g[n];
+                    }
+                    dys[(int64_t)p[j] * per_row + v] = pack<T, VEC>(d);
+                }
             }
         }
 #pragma unroll
-        for (int j = 0; j < kBwdSlots; ++j) {
+        for (int j = 0; j < S; ++j) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
+            if (lane == 0) part[warp][j] = dot[j];
         }
-        __syncthreads();
-        if (threadIdx.x < kBwdSlots && j0 + (int)threadIdx.x < k) {
+        if (W > 1) __syncthreads();
+        else __syncwarp();
+        if (at < S && j0 + at < k && live) {
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kBwdThreads / 32; ++i) sum += part[i][threadIdx.x];
-            dweights[s0 + j0 + threadIdx.x] = sum;
+            for (int i = 0; i < W; ++i) sum += part[W > 1 ? i : warp][at];
+            dweights[s0 + j0 + at] = sum;
         }
-        __syncthreads();
+        if (W > 1) __syncthreads();
+        else __syncwarp();
     }
 }
 
@@ -307,14 +381,20 @@ inline unsigned row_grid(int64_t rows, int64_t chunks) {
 template <typename T>
 cudaError_t sort_launch(const void *ids, int64_t R, int k, int E, int32_t *tokens, int32_t *pos, int32_t *offsets,
                         cudaStream_t st) {
-    const size_t smem = ((size_t)kSortWarps * E + E + E + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    // up to two chunks a warp one CTA is done sooner than eight can meet
+    // one CTA while its warps have two chunks of 32 slots or fewer: eight take longer to meet
     const unsigned ctas = R <= 2 * 32 * kSortWarps ? 1 : kSortCtas;
+    // and no more warps than chunks: every warp's histogram costs its clearing and its sum
+    const int64_t chunks = (R + 31) / 32;
+    const int warps = chunks >= kSortWarps ? kSortWarps : chunks < 4 ? 4 : (int)chunks;
+    const size_t smem = ((size_t)warps * E + 3 * (size_t)E + 1) * 4;
+    auto kern = moe_sort_kernel<T>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kSortThreads);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at;
@@ -323,39 +403,93 @@ cudaError_t sort_launch(const void *ids, int64_t R, int k, int E, int32_t *token
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_sort_kernel<T>, static_cast<const T *>(ids), R, k, E, tokens, pos, offsets);
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T *>(ids), R, k, E, tokens, pos, offsets);
+}
+
+// Parts of 32 accesses that a warp takes of a row of per_row accesses: at most `most`, a power of 2.
+inline int row_parts(int64_t per_row, int most) {
+    int p = 1;
+    while (p < most && 32 * (int64_t)p < per_row) p *= 2;
+    return p;
+}
+
+template <typename V>
+cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64_t R, int64_t per_row, void *xs,
+                          cudaStream_t st, bool *fits) {
+    const int P = row_parts(per_row, kInFlight);
+    const int64_t chunks = (per_row + 32 * P - 1) / (32 * P), groups = (R + kInFlight / P - 1) / (kInFlight / P);
+    const unsigned grid = row_grid(groups, chunks);
+    *fits = grid != 0;
+    if (!grid) return cudaSuccess;
+#define Q4_GATHER(P_)                                                                                              \
+    moe_gather_kernel<V, P_><<<grid, 256, 0, st>>>(static_cast<const V *>(x), T, tokens, R, per_row, (uint32_t)chunks, \
+                                                   static_cast<V *>(xs))
+    if (P == 1) Q4_GATHER(1);
+    else if (P == 2) Q4_GATHER(2);
+    else if (P == 4) Q4_GATHER(4);
+    else Q4_GATHER(8);
+#undef Q4_GATHER
+    return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t combine_rows(const void *ys, int64_t R, const int32_t *pos, const float *weights, int64_t tokens, int k,
+                         int64_t per_row, void *out, cudaStream_t st, bool *fits) {
+    using V = typename Row<T, VEC>::V;
+    // slots times parts of a row: eight accesses on their way where the row is long enough
+    const int P = row_parts(per_row, k == 1 ? 8 : k == 2 ? 4 : 2);
+    const int64_t chunks = (per_row + 32 * P - 1) / (32 * P);
+    const unsigned grid = row_grid(tokens, chunks);
+    *fits = grid != 0;
+    if (!grid) return cudaSuccess;
+#define Q4_COMBINE(S_, P_)                                                                                            \
+    moe_combine_kernel<T, VEC, S_, P_><<<grid, 256, 0, st>>>(static_cast<const V *>(ys), R, pos, weights, tokens, k, \
+                                                             per_row, (uint32_t)chunks, static_cast<V *>(out))
+    if (P == 8) Q4_COMBINE(1, 8);
+    else if (P == 4) Q4_COMBINE(2, 4);
+    else if (P == 2) Q4_COMBINE(4, 2);
+    else Q4_COMBINE(8, 1);
+#undef Q4_COMBINE
+    return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t combine_launch(const void *ys, int64_t R, const int32_t *pos, const float *weights, int64_t tokens, int k,
                            int64_t D, void *out, cudaStream_t st, bool *fits) {
-    const bool vec = (D * (int64_t)sizeof(T)) % 16 == 0 && aligned16(ys) && aligned16(out);
-    const int64_t per_row = vec ? D * (int64_t)sizeof(T) / 16 : D, chunks = (per_row + 31) / 32;
-    const unsigned grid = row_grid(tokens, chunks);
-    *fits = grid != 0;
-    if (!grid) return cudaSuccess;
-    if (vec)
-        moe_combine_kernel<T, true><<<grid, 256, 0, st>>>(static_cast<const uint4 *>(ys), R, pos, weights, tokens, k,
-                                                          per_row, (uint32_t)chunks, static_cast<uint4 *>(out));
-    else
-        moe_combine_kernel<T, false><<<grid, 256, 0, st>>>(static_cast<const T *>(ys), R, pos, weights, tokens, k,
-                                                           per_row, (uint32_t)chunks, static_cast<T *>(out));
+    const int64_t bytes = D * (int64_t)sizeof(T);
+    if (bytes % 16 == 0 && aligned16(ys) && aligned16(out))
+        return combine_rows<T, true>(ys, R, pos, weights, tokens, k, bytes / 16, out, st, fits);
+    return combine_rows<T, false>(ys, R, pos, weights, tokens, k, D, out, st, fits);
+}
+
+template <typename T, bool VEC>
+cudaError_t bwd_rows(const void *dout, const void *ys, int64_t R, const int32_t *pos, const float *weights,
+                     int64_t tokens, int k, int64_t per_row, void *dys, float *dweights, cudaStream_t st) {
+    using V = typename Row<T, VEC>::V;
+#define Q4_BWD(W_, S_, P_)                                                                                             \
+    moe_combine_bwd<T, VEC, W_, S_, P_><<<(unsigned)((tokens + 4 / W_ - 1) / (4 / W_)), 128, 0, st>>>(                 \
+        static_cast<const V *>(dout), static_cast<const V *>(ys), R, pos, weights, tokens, k, per_row,                 \
+        static_cast<V *>(dys), dweights)
+    // rows below 128 accesses leave three of four warps idle: one warp a token there
+    // (65536 tokens x 8 of 256 bf16 values: 290 us with four)
+    if (per_row >= 128) {
+        if (k <= 2) Q4_BWD(4, 2, 4);
+        else Q4_BWD(4, 8, 1);
+    } else {
+        if (k <= 2) Q4_BWD(1, 2, 2);
+        else Q4_BWD(1, 8, 1);
+    }
+#undef Q4_BWD
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t bwd_launch(const void *dout, const void *ys, int64_t R, const int32_t *pos, const float *weights,
                        int64_t tokens, int k, int64_t D, void *dys, float *dweights, cudaStream_t st) {
-    const bool vec = (D * (int64_t)sizeof(T)) % 16 == 0 && aligned16(ys) && aligned16(dout) && aligned16(dys);
-    if (vec)
-        moe_combine_bwd<T, true><<<(unsigned)tokens, kBwdThreads, 0, st>>>(
-            static_cast<const uint4 *>(dout), static_cast<const uint4 *>(ys), R, pos, weights, k,
-            D * (int64_t)sizeof(T) / 16, static_cast<uint4 *>(dys), dweights);
-    else
-        moe_combine_bwd<T, false><<<(unsigned)tokens, kBwdThreads, 0, st>>>(
-            static_cast<const T *>(dout), static_cast<const T *>(ys), R, pos, weights, k, D, static_cast<T *>(dys),
-            dweights);
-    return cudaGetLastError();
+    const int64_t bytes = D * (int64_t)sizeof(T);
+    if (bytes % 16 == 0 && aligned16(ys) && aligned16(dout) && aligned16(dys))
+        return bwd_rows<T, true>(dout, ys, R, pos, weights, tokens, k, bytes / 16, dys, dweights, st);
+    return bwd_rows<T, false>(dout, ys, R, pos, weights, tokens, k, D, dys, dweights, st);
 }
 
 // Shapes that every call below shares: slots and rows in 32 bits.
@@ -393,21 +527,14 @@ q4_status q4_moe_gather(const void *x, q4_dtype xt, int64_t T, int64_t D, const 
     if (R == 0 || T == 0) return Q4_OK;
     if (!x || !tokens || !xs) return Q4_ERR_ARG;
     const int64_t bytes = D * q4::elem_size(xt);
-    const bool vec = bytes % 16 == 0 && q4::aligned16(x) && q4::aligned16(xs);
-    const int64_t per_row = vec ? bytes / 16 : D, chunks = (per_row + 32 * q4::kGatherVecs - 1) / (32 * q4::kGatherVecs);
-    const unsigned grid = q4::row_grid(R, chunks);
-    if (!grid) return Q4_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (vec)
-        q4::moe_gather_kernel<uint4><<<grid, 256, 0, st>>>(static_cast<const uint4 *>(x), T, tokens, R, per_row,
-                                                           (uint32_t)chunks, static_cast<uint4 *>(xs));
-    else if (xt == Q4_F32)
-        q4::moe_gather_kernel<uint32_t><<<grid, 256, 0, st>>>(static_cast<const uint32_t *>(x), T, tokens, R, per_row,
-                                                              (uint32_t)chunks, static_cast<uint32_t *>(xs));
-    else
-        q4::moe_gather_kernel<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(x), T, tokens, R, per_row,
-                                                              (uint32_t)chunks, static_cast<uint16_t *>(xs));
-    return q4::cuda_error(cudaGetLastError(), "moe_gather launch");
+    bool fits = true;
+    const cudaError_t e = bytes % 16 == 0 && q4::aligned16(x) && q4::aligned16(xs)
+                              ? q4::gather_launch<uint4>(x, T, tokens, R, bytes / 16, xs, st, &fits)
+                          : xt == Q4_F32 ? q4::gather_launch<uint32_t>(x, T, tokens, R, D, xs, st, &fits)
+                                         : q4::gather_launch<uint16_t>(x, T, tokens, R, D, xs, st, &fits);
+    if (!fits) return Q4_ERR_UNSUPPORTED;
+    return q4::cuda_error(e, "moe_gather launch");
 }
 
 q4_status q4_moe_combine(const void *ys, q4_dtype yt, int64_t R, int64_t D, const int32_t *pos, const float *weights,
