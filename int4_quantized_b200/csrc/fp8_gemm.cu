@@ -6,7 +6,7 @@
 // fp32 sums in tensor memory); each block's sum is then multiplied by its two scales and
 // added in fp32 registers ("promotion"), and y is rounded once.
 //
-// Few rows (fp8_stream): A = 128 weight rows, B = 16 to 128 rows of x, so that the weights,
+// Few rows (fp8_stream): A = 128 weight rows, B = 16 to 64 rows of x, so that the weights,
 // which are nearly all the bytes, fill the tensor core's long side; D = 128 lanes (weight
 // rows) x NT columns (rows of x). K is split over a thread-block cluster where the tiles
 // alone would leave SMs without work; the CTAs then exchange their partial sums through
@@ -149,8 +149,8 @@ Q4_DEVINL uint32_t map_rank(uint32_t smem_addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
     return r;
 }
-Q4_DEVINL void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+Q4_DEVINL void st_cluster2(uint32_t addr, float a, float b) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 Q4_DEVINL void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -162,6 +162,9 @@ Q4_DEVINL void arrive_peer(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 Q4_DEVINL void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+Q4_DEVINL void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+Q4_DEVINL void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+Q4_DEVINL void prefetch_map(const void *tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
 Q4_DEVINL void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -171,11 +174,11 @@ template <int NT>
 struct Stream {
     static constexpr int kXBytes = NT * kBK;
     static constexpr int kStage = kWBytes + kXBytes;
-    static constexpr int kBufs = NT <= 64 ? 8 : 4;       // tensor-memory buffers of NT columns
+    static constexpr int kBufs = 8;                      // tensor-memory buffers of NT columns
     static constexpr int kCols = kBufs * NT;             // 128 to 512 columns
     // one warp an SM quarter adds up to 32 columns a block of k before the next block's sums
-    // are there; wider tiles take two (NT = 128 with one: 0.9 us a block, its loads and waits
-    // one after the other)
+    // are there; wider tiles take two (with one, 128 columns took 0.9 us a block, the loads and
+    // waits one after the other)
     static constexpr int kEpiWarps = NT <= 32 ? 4 : 8;
     static constexpr int kOwn = NT * 4 / kEpiWarps;      // columns a warp keeps
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
@@ -194,7 +197,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *p = ring + (size_t)a.stages * S::kStage;
-    float *parts = reinterpret_cast<float *>(p);  // [split][NT / split][128]
+    float *parts = reinterpret_cast<float *>(p);  // [split][NT / split / 2][128][2]
     if (a.split > 1) p += kWRows * NT * 4;
     float *xsc = reinterpret_cast<float *>(p);  // [kBufs][NT]
     uint64_t *full = reinterpret_cast<uint64_t *>(p + S::kBufs * NT * 4);
@@ -209,6 +212,10 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     int32_t *rows0 = first + a.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        prefetch_map(&tmw);
+        prefetch_map(&tmx);
+    }
     if (threadIdx.x == 32) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(full + i, 1);
@@ -231,7 +238,8 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     count_tiles(a, NT, first, rows0);
     tc_fence_before();
     __syncthreads();
-    if (a.split > 1) cluster_sync_all();  // every CTA's barriers stand before another arrives on them
+    // every CTA's barriers must stand before another arrives on them: waited for before the exchange
+    if (a.split > 1) cluster_arrive();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -239,6 +247,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     const int64_t tiles = (int64_t)first[a.E] * a.nb;
     // a split tile is its cluster's only one: the exchange buffer is used once
     const int64_t step = a.split > 1 ? tiles : gridDim.x, tile0 = blockIdx.x / a.split;
+    bool met = false;  // this thread has waited for the cluster
     const int k0 = (int)((int64_t)a.kb * rank / a.split), k1 = (int)((int64_t)a.kb * (rank + 1) / a.split);
     bool timed_out = false;
 
@@ -369,27 +378,29 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
                         if (c0 + c < t.rows) y[(int64_t)(t.row0 + c0 + c) * a.N + n] = round_to<Y>(value(c));
                 }
             } else {
-                // column c is added and stored by CTA c / (NT / split); slot r holds CTA r's part
-                const int cols = NT / a.split;
+                // Columns are added and stored by CTA column / (NT / split); slot r of its buffer
+                // holds CTA r's part, two columns of a row side by side (each CTA has two or more)
+                // and the rows of such a pair one after the other: no bank is written twice.
+                const int shift = __ffs(NT / a.split) - 1, cols = 1 << shift;
+                cluster_wait();
+                met = true;
 #pragma unroll
-                for (int c = 0; c < OWN; ++c) {
-                    const int to = (c0 + c) / cols, in = c0 + c - to * cols;
-                    st_cluster(map_rank(smem_u32(parts + ((int64_t)rank * cols + in) * kWRows + rl), (uint32_t)to),
-                               value(c));
+                for (int c = 0; c < OWN; c += 2) {
+                    const int to = (c0 + c) >> shift, in = (c0 + c) & (cols - 1);
+                    st_cluster2(map_rank(smem_u32(parts + ((((rank << shift) + in) << 6) + rl) * 2), (uint32_t)to), value(c),
+                                value(c + 1));
                 }
                 fence_cluster();
                 __syncwarp();
-                if (lane == 0) {
-                    for (int r = 0; r < a.split; ++r) arrive_cluster(map_rank(smem_u32(joined), (uint32_t)r));
-                }
+                if (lane < a.split) arrive_cluster(map_rank(smem_u32(joined), (uint32_t)lane));
                 timed_out |= !mbar_wait(joined, 0);
                 fence_cluster();
                 if (n < a.N && !timed_out) {
                     for (int in = (warp - 4) >> 2; in < cols; in += S::kEpiWarps / 4) {
-                        const int c = rank * cols + in;
+                        const int c = (rank << shift) + in;
                         if (c >= t.rows) break;
                         float sum = 0.f;
-                        for (int r = 0; r < a.split; ++r) sum += parts[((int64_t)r * cols + in) * kWRows + rl];
+                        for (int r = 0; r < a.split; ++r) sum += parts[((((r << shift) + (in & ~1)) << 6) + rl) * 2 + (in & 1)];
                         y[(int64_t)(t.row0 + c) * a.N + n] = round_to<Y>(sum);
                     }
                 }
@@ -400,8 +411,12 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    // a CTA of a cluster may go only when no other can still write to it
-    if (a.split > 1) cluster_sync_all();
+    if (a.split > 1) {
+        if (!met) cluster_wait();
+        // A CTA whose parts have all come cannot be written to any more. One that gave up on
+        // them stays until the others have gone or given up too.
+        if (__syncthreads_or(timed_out)) cluster_sync_all();
+    }
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, S::kCols);
 }
@@ -463,6 +478,10 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
+    if (threadIdx.x == 0) {
+        prefetch_map(&tmw);
+        prefetch_map(&tmx);
+    }
     if (threadIdx.x == 32) {
         for (int i = 0; i < W::kStages; ++i) {
             mbar_init(full + i, 1);
@@ -702,8 +721,7 @@ cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int
     const int64_t typical = a.offsets ? std::min((int64_t)a.R, 2 * (((int64_t)a.R + a.E - 1) / a.E)) : a.R;
     if (typical <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
     if (typical <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
-    if (typical <= 64) return launch_stream<64, Y>(a, x, w, K, sms, st);
-    if (typical <= 128) return launch_stream<128, Y>(a, x, w, K, sms, st);
+    if (typical <= (a.offsets ? 96 : 64)) return launch_stream<64, Y>(a, x, w, K, sms, st);
     return launch_wide<256, Y>(a, x, w, K, sms, st);
 }
 

@@ -28,26 +28,42 @@ def _dtype(t: torch.dtype, name: str) -> int:
     return _DTYPES[t]
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Optional[int]:
-    """Device pointer of a contiguous CUDA tensor of this dtype and shape on this device (None stays None)."""
-    if t is None:
-        return None
-    _cuda(t, name, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _arg(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """Device pointer of a contiguous CUDA tensor of this dtype and shape (None: any) on this device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.device != device or (
+            shape is not None and t.shape != shape):
+        _cuda(t, name, dtype)
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
         raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
+def _new(shape, dtype, device) -> torch.Tensor:
+    """A contiguous tensor, uninitialised (strided: the quickest of torch's ways to make one)."""
+    if len(shape) == 2:
+        stride = (shape[1] or 1, 1)
+    else:
+        stride, n = [], 1
+        for d in reversed(shape):
+            stride.append(n)
+            n *= d or 1
+        stride.reverse()
+    return torch.empty_strided(shape, stride, dtype=dtype, device=device)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
+
+
 def _call(device: torch.device, what: str, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, with the device current."""
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, stream)
+    i = device.index
+    if _current() == i:
+        code = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(device):
-            code = fn(*args, stream)
+            code = fn(*args, _raw_stream(i))
     if code:
         _check(code, what)
 
@@ -57,10 +73,11 @@ def _blocks(n: int) -> int:
 
 
 def _status(status: Optional[torch.Tensor], device) -> Optional[int]:
-    p = _arg(status, "status", torch.int32, None, device)
-    if status is not None and status.numel() < 1:
+    if status is None:
+        return None
+    if status.numel() < 1:
         raise ValueError("status must hold one int32")
-    return p
+    return _arg(status, "status", torch.int32, None, device)
 
 
 def fp8_pack(x: torch.Tensor, rows: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
@@ -88,13 +105,15 @@ def fp8_pack(x: torch.Tensor, rows: Optional[torch.Tensor] = None, count: Option
         rp = _arg(rows, "rows", torch.int32, None, dev)
         R = rows.shape[0]
         lead = (R,)
-    cp = _arg(count, "count", torch.int32, None, dev)
-    if count is not None and count.numel() < 1:
-        raise ValueError("count must hold one int32")
+    cp = None
+    if count is not None:
+        cp = _arg(count, "count", torch.int32, None, dev)
+        if count.numel() < 1:
+            raise ValueError("count must hold one int32")
     if codes is None:
-        codes = torch.empty((*lead, K), dtype=E4M3, device=dev)
+        codes = _new((*lead, K), E4M3, dev)
     if scales is None:
-        scales = torch.empty((*lead, _blocks(K)), dtype=torch.float32, device=dev)
+        scales = _new((*lead, _blocks(K)), torch.float32, dev)
     _call(dev, "fp8_pack", lib().q4_fp8_pack, x.data_ptr(), xt, n, K, rp, R, cp, FP8_PACK_SILU_MUL if silu_mul else 0,
           _arg(codes, "codes", E4M3, (*lead, K), dev), _arg(scales, "scales", torch.float32, (*lead, _blocks(K)), dev),
           _status(status, dev))
@@ -115,9 +134,9 @@ def fp8_pack_weights(w: torch.Tensor, codes: Optional[torch.Tensor] = None, scal
         E *= d
     sshape = (*w.shape[:-2], _blocks(N), _blocks(K))
     if codes is None:
-        codes = torch.empty(w.shape, dtype=E4M3, device=dev)
+        codes = _new(w.shape, E4M3, dev)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+        scales = _new(sshape, torch.float32, dev)
     _call(dev, "fp8_pack_weights", lib().q4_fp8_pack_weights, w.data_ptr(), wt, E, N, K,
           _arg(codes, "codes", E4M3, w.shape, dev), _arg(scales, "scales", torch.float32, sshape, dev),
           _status(status, dev))
@@ -135,13 +154,13 @@ def fp8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales:
     N, K = w.shape
     lead = tuple(x.shape[:-1])
     if out is None:
-        out = torch.empty((*lead, N), dtype=out_dtype, device=dev)
+        out = _new((*lead, N), out_dtype, dev)
     yt = _dtype(out.dtype, "out")
     kb = _blocks(K)
     _call(dev, "fp8_gemm", lib().q4_fp8_gemm, x.data_ptr(),
           _arg(x_scales, "x_scales", torch.float32, (*lead, kb), dev), x.numel() // K, _arg(w, "w", E4M3, None, dev),
           _arg(w_scales, "w_scales", torch.float32, (_blocks(N), kb), dev), N, K,
-          _arg(out, "out", None, (*lead, N), dev), yt, _status(status, dev))
+          _arg(out, "out", out.dtype, (*lead, N), dev), yt, _status(status, dev))
     return out
 
 
@@ -160,12 +179,12 @@ def fp8_gemm_grouped(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w
     R = x.shape[0]
     E, N, K = w.shape
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        out = _new((R, N), out_dtype, dev)
     yt = _dtype(out.dtype, "out")
     kb = _blocks(K)
     _call(dev, "fp8_gemm_grouped", lib().q4_fp8_gemm_grouped, x.data_ptr(),
           _arg(x_scales, "x_scales", torch.float32, (R, kb), dev), R,
           _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E, _arg(w, "w", E4M3, None, dev),
           _arg(w_scales, "w_scales", torch.float32, (E, _blocks(N), kb), dev), N, K,
-          _arg(out, "out", None, (R, N), dev), yt, _status(status, dev))
+          _arg(out, "out", out.dtype, (R, N), dev), yt, _status(status, dev))
     return out

@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _cuda, lib
-from .fp8 import E4M3, _arg, _blocks, _call, _dtype, fp8_gemm_grouped, fp8_pack, fp8_pack_weights
+from .fp8 import E4M3, _arg, _blocks, _call, _dtype, _new, fp8_gemm_grouped, fp8_pack, fp8_pack_weights
 
 
 def moe_sort(ids: torch.Tensor, num_experts: int) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
@@ -39,9 +39,7 @@ def moe_sort(ids: torch.Tensor, num_experts: int) -> Tuple[torch.Tensor, torch.T
     if E < 1:
         raise ValueError("num_experts must be at least 1")
     dev = ids.device
-    # one allocation for the three
-    buf = torch.empty(2 * T * k + E + 1, dtype=torch.int32, device=dev)
-    tokens, pos, offsets = buf[:T * k], buf[T * k:2 * T * k].view(T, k), buf[2 * T * k:]
+    tokens, pos, offsets = _new((T * k,), torch.int32, dev), _new((T, k), torch.int32, dev), _new((E + 1,), torch.int32, dev)
     _call(dev, "moe_sort", lib().q4_moe_sort, ids.data_ptr(), 32 if ids.dtype == torch.int32 else 64, T, k, E,
           tokens.data_ptr(), pos.data_ptr(), offsets.data_ptr())
     return tokens, pos, offsets
@@ -57,7 +55,7 @@ def moe_gather(x: torch.Tensor, tokens: torch.Tensor, out: Optional[torch.Tensor
     T, D = x.shape
     R = tokens.shape[0]
     if out is None:
-        out = torch.empty((R, D), dtype=x.dtype, device=dev)
+        out = _new((R, D), x.dtype, dev)
     _call(dev, "moe_gather", lib().q4_moe_gather, x.data_ptr(), xt, T, D, _arg(tokens, "tokens", torch.int32, None, dev),
           R, _arg(out, "out", x.dtype, (R, D), dev))
     return out
@@ -74,9 +72,10 @@ def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Ten
     R, D = ys.shape
     T, k = pos.shape
     if out is None:
-        out = torch.empty((T, D), dtype=ys.dtype, device=dev)
+        out = _new((T, D), ys.dtype, dev)
     _call(dev, "moe_combine", lib().q4_moe_combine, ys.data_ptr(), yt, R, D, _arg(pos, "pos", torch.int32, None, dev),
-          _arg(weights, "weights", torch.float32, (T, k), dev), T, k, _arg(out, "out", ys.dtype, (T, D), dev))
+          None if weights is None else _arg(weights, "weights", torch.float32, (T, k), dev), T, k,
+          _arg(out, "out", ys.dtype, (T, D), dev))
     return out
 
 
@@ -97,8 +96,8 @@ def moe_combine_backward(dout: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor
     R, D = ys.shape
     T, k = pos.shape
     if dys is None:
-        dys = torch.empty((R, D), dtype=ys.dtype, device=dev)
-    dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        dys = _new((R, D), ys.dtype, dev)
+    dweights = _new((T, k), torch.float32, dev)
     _call(dev, "moe_combine_backward", lib().q4_moe_combine_backward, _arg(dout, "dout", ys.dtype, (T, D), dev),
           ys.data_ptr(), yt, R, D, _arg(pos, "pos", torch.int32, None, dev),
           _arg(weights, "weights", torch.float32, (T, k), dev), T, k, _arg(dys, "dys", ys.dtype, (R, D), dev),
