@@ -16,15 +16,15 @@
 //   warp 2      the rows' scales of each block, by 4-byte asynchronous copies
 //   warps 4-..  promotion and stores; lane = weight row, so stores of y are contiguous
 //
-// Many rows (fp8_wide): a pair of CTAs (cta_group::2) makes one tile of 256 rows of x x BN
-// weight rows. Each CTA loads its own 128 rows of x and half of the weights, so a block of k
-// costs each SM 128 + BN / 2 rows of 128 bytes instead of 128 + BN: at 256 x 256 a single CTA
-// would have to bring 96 bytes a clock from L2, above the 64 an SM can take. Here D's lanes
-// are rows of x, so that the scale of a thread's whole row of D is one number a block of k.
-//   warp 0      TMA producer (both CTAs; all bytes are counted on the first CTA's barriers)
-//   warp 1      tensor memory; in the first CTA, MMA issue for both
-//   warps 4-11  promotion and stores: 32 rows x BN / 2 columns a warp, kept in registers;
-//               the first four warps give theirs up to them (setmaxnreg)
+// Many rows (fp8_wide): one CTA makes a tile of 128 rows of x x 256 weight rows, or a pair of
+// CTAs (cta_group::2) one of 256 x 256. In a pair each CTA loads its own rows of x and half of
+// the weights, so that a block of k costs an SM 32 KB from L2 instead of 48; single CTAs leave
+// fewer rows of a tile empty. Here D's lanes are rows of x, so that the scale of a thread's
+// whole row of D is one number a block of k.
+//   warp 0      TMA producer (of a pair both; all bytes are counted on the first CTA's barriers)
+//   warp 1      tensor memory; MMA issue (in the first CTA, for both)
+//   warps 4-11  promotion and stores: 32 rows x 128 columns a warp, kept in registers; the
+//               first four warps give theirs up to them (setmaxnreg)
 // Every wait is bounded (about one second); one that gives up sets Q4_STATUS_TIMEOUT in the
 // status word, and the roles run to completion without further waits.
 #include <cuda.h>
@@ -422,7 +422,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
 }
 
 // ---- many rows ----------------------------------------------------------------------------
-constexpr int kWideRows = 256;     // rows of x a pair
+constexpr int kWideCols = 256;     // weight rows a tile
 constexpr int kWideThreads = 384;  // TMA, MMA, two without a role, eight epilogue warps
 // The block launches with 168 registers a thread; the first warpgroup keeps 72, the two
 // epilogue warpgroups (128 fp32 sums a thread) take 216: 128 * 72 + 256 * 216 is exactly the
@@ -430,18 +430,31 @@ constexpr int kWideThreads = 384;  // TMA, MMA, two without a role, eight epilog
 constexpr int kWideRegs = 168, kWideLow = 72, kWideHigh = 216;
 static_assert(128 * kWideLow + 256 * kWideHigh == kWideThreads * kWideRegs, "register split");
 
-template <int BN>
+template <bool PAIR>
 struct Wide {
+    static constexpr int kCtas = PAIR ? 2 : 1;
+    static constexpr int kRows = 128 * kCtas;        // rows of x a tile
+    static constexpr int kOwnCols = kWideCols / kCtas;  // weight rows that a CTA loads
     static constexpr int kXBytes = 128 * kBK;
-    static constexpr int kBBytes = BN / 2 * kBK;
-    static constexpr int kStage = kXBytes + kBBytes;
-    static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 8 of 24 KB
-    static constexpr int kBufs = 512 / BN;           // all 512 columns of tensor memory
-    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kWideRows >> 4) << 24);
+    static constexpr int kStage = kXBytes + kOwnCols * kBK;
+    static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 4 of 48 KB
+    static constexpr int kBufs = 512 / kWideCols;    // all 512 columns of tensor memory
+    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kWideCols >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
     static size_t smem(int E) {
         return 1024 + (size_t)kStages * kStage + (2 * kStages + 2 * kBufs + 1) * 8 + 16 + (size_t)(2 * E + 2) * 4;
     }
 };
+
+template <bool PAIR>
+Q4_DEVINL void umma_f8_of(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    if constexpr (PAIR) umma_f8_pair(d, ad, bd, idesc, acc);
+    else umma_f8(d, ad, bd, idesc, acc);
+}
+template <bool PAIR>
+Q4_DEVINL void umma_commit_of(uint64_t *bar) {
+    if constexpr (PAIR) umma_commit_pair(bar);
+    else umma_commit(bar);
+}
 
 // 32 bytes in one store: a whole sector, although neighbouring lanes write different rows.
 Q4_DEVINL void st_v8(void *p, const uint32_t (&v)[8]) {
@@ -460,11 +473,11 @@ Q4_DEVINL uint32_t two(float lo, float hi) {
     }
 }
 
-template <int BN, typename Y>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+template <bool PAIR, typename Y>
+__global__ void __launch_bounds__(kWideThreads, 1)
 fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw) {
-    using W = Wide<BN>;
-    constexpr int HALF = BN / 2;  // columns an epilogue warp keeps
+    using W = Wide<PAIR>;
+    constexpr int HALF = kWideCols / 2;  // columns an epilogue warp keeps
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + W::kStages * W::kStage);
@@ -477,7 +490,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
     int32_t *rows0 = first + a.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
+    const int rank = PAIR ? (int)cluster_rank() : 0;
     if (threadIdx.x == 0) {
         prefetch_map(&tmw);
         prefetch_map(&tmx);
@@ -489,24 +502,29 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
         }
         for (int i = 0; i < W::kBufs; ++i) {
             mbar_init(dfull + i, 1);
-            mbar_init(dempty + i, 16);  // the epilogue warps of both CTAs
+            mbar_init(dempty + i, 8 * W::kCtas);  // the epilogue warps (of both CTAs)
         }
         mbar_init(done, 1);
         fence_barrier_init();
     }
     if (warp == 1) {
         __syncwarp();
-        tmem_alloc2(tmem_slot, 512);
-        tmem_relinquish2();
+        if constexpr (PAIR) {
+            tmem_alloc2(tmem_slot, 512);
+            tmem_relinquish2();
+        } else {
+            tmem_alloc(tmem_slot, 512);
+            tmem_relinquish();
+        }
     }
-    count_tiles(a, kWideRows, first, rows0);
+    count_tiles(a, W::kRows, first, rows0);
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int cols = (int)((a.N + BN - 1) / BN);
-    const int64_t tiles = (int64_t)first[a.E] * cols, step = gridDim.x / 2;
+    const int cols = (int)((a.N + kWideCols - 1) / kWideCols);
+    const int64_t tiles = (int64_t)first[a.E] * cols, step = gridDim.x / W::kCtas, tile0 = blockIdx.x / W::kCtas;
     bool timed_out = false;
 
     if (warp < 4) {
@@ -515,19 +533,24 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             if (lane == 0) {
                 Slot s;
                 int filled = 0;
-                for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
-                    const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
-                    const int wrow = (int)(t.e * a.N + (int64_t)t.nb * BN + rank * HALF);
+                for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+                    const Tile t = tile_at(a, W::kRows, cols, first, rows0, j);
+                    const int wrow = (int)(t.e * a.N + (int64_t)t.nb * kWideCols + rank * W::kOwnCols);
                     const int xrow = t.row0 + rank * 128;
                     for (int kb = 0; kb < a.kb; ++kb) {
                         timed_out = !mbar_wait(empty + s.i, s.round ^ 1);
                         if (timed_out) break;
-                        // the first CTA's barrier counts the bytes of both
-                        if (rank == 0) mbar_arrive_expect_tx(full + s.i, 2 * W::kStage);
-                        const uint32_t bar = map_rank(smem_u32(full + s.i), 0);
                         uint8_t *st = ring + s.i * W::kStage;
-                        tma_load_2d_pair(st, &tmx, bar, kb * kBK, xrow);
-                        tma_load_2d_pair(st + W::kXBytes, &tmw, bar, kb * kBK, wrow);
+                        // of a pair, the first CTA's barrier counts the bytes of both
+                        if (rank == 0) mbar_arrive_expect_tx(full + s.i, W::kCtas * W::kStage);
+                        if constexpr (PAIR) {
+                            const uint32_t bar = map_rank(smem_u32(full + s.i), 0);
+                            tma_load_2d_pair(st, &tmx, bar, kb * kBK, xrow);
+                            tma_load_2d_pair(st + W::kXBytes, &tmw, bar, kb * kBK, wrow);
+                        } else {
+                            tma_load_2d(st, &tmx, full + s.i, kb * kBK, xrow);
+                            tma_load_2d(st + W::kXBytes, &tmw, full + s.i, kb * kBK, wrow);
+                        }
                         s.next(W::kStages);
                         filled = min(filled + 1, W::kStages);
                     }
@@ -542,7 +565,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             Slot s, d;
             const uint64_t base = sw128_desc(ring);
             const uint32_t dt = __shfl_sync(0xffffffffu, tmem, 0);
-            for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
+            for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
                 for (int kb = 0; kb < a.kb; ++kb) {
                     timed_out = !mbar_wait(dempty + d.i, d.round ^ 1);
                     if (!timed_out) timed_out = !mbar_wait(full + s.i, s.round);
@@ -553,16 +576,17 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)
-                            umma_f8_pair(dt + (uint32_t)(d.i * BN), xd + 2 * kk, wd + 2 * kk, W::kIdesc, kk > 0 ? 1u : 0u);
-                        umma_commit_pair(empty + s.i);
-                        umma_commit_pair(dfull + d.i);
+                            umma_f8_of<PAIR>(dt + (uint32_t)(d.i * kWideCols), xd + 2 * kk, wd + 2 * kk, W::kIdesc,
+                                             kk > 0 ? 1u : 0u);
+                        umma_commit_of<PAIR>(empty + s.i);
+                        umma_commit_of<PAIR>(dfull + d.i);
                     }
                     __syncwarp();
                     s.next(W::kStages);
                     d.next(W::kBufs);
                 }
             }
-            if (elect_one()) umma_commit_pair(done);
+            if (elect_one()) umma_commit_of<PAIR>(done);
             __syncwarp();
             timed_out |= !mbar_wait(done, 0);
         }
@@ -574,11 +598,11 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
         constexpr int PER = 32 / (int)sizeof(Y);  // values a 32-byte store
         const bool vec = a.N % PER == 0 && (uintptr_t)a.y % 32 == 0;
         Slot d;
-        for (int64_t j = blockIdx.x / 2; j < tiles && !timed_out; j += step) {
-            const Tile t = tile_at(a, kWideRows, cols, first, rows0, j);
+        for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
+            const Tile t = tile_at(a, W::kRows, cols, first, rows0, j);
             const int rl = rank * 128 + 32 * q + lane;  // row inside the tile
             const bool live = rl < t.rows;
-            const int64_t n0 = (int64_t)t.nb * BN + half * HALF;
+            const int64_t n0 = (int64_t)t.nb * kWideCols + half * HALF;
             const float *xsc = a.xs + (int64_t)(t.row0 + min(rl, t.rows - 1)) * a.kb;
             const float *wsc = a.ws + ((int64_t)t.e * a.nb + min((int)(n0 / 128), a.nb - 1)) * a.kb;
             uint64_t acc[HALF / 2];
@@ -595,13 +619,16 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32) {
                     uint32_t v0[16], v1[16];
-                    tmem_ld16(lane_base + (uint32_t)(d.i * BN + c), v0);
-                    tmem_ld16(lane_base + (uint32_t)(d.i * BN + c + 16), v1);
+                    tmem_ld16(lane_base + (uint32_t)(d.i * kWideCols + c), v0);
+                    tmem_ld16(lane_base + (uint32_t)(d.i * kWideCols + c + 16), v1);
                     tmem_wait_ld();
                     if (c + 32 == HALF) {  // all read: the buffer is free
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_peer(map_rank(smem_u32(dempty + d.i), 0));
+                        if (lane == 0) {
+                            if constexpr (PAIR) arrive_peer(map_rank(smem_u32(dempty + d.i), 0));
+                            else mbar_arrive(dempty + d.i);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -638,9 +665,12 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // neither CTA goes while the other may still reach into it
+    if constexpr (PAIR) cluster_sync_all();  // neither CTA goes while the other may still reach into it
     tc_fence_after();
-    if (warp == 1) tmem_dealloc2(tmem, 512);
+    if (warp == 1) {
+        if constexpr (PAIR) tmem_dealloc2(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
 }
 
 // ---- host ---------------------------------------------------------------------------------
@@ -656,14 +686,17 @@ bool encode_codes_map(CUtensorMap *tm, const uint8_t *codes, int64_t rows, int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Row tiles of `rows` rows: at most (which experts have rows is known on the device only).
+int64_t row_tiles(const Fp8Args &a, int rows) {
+    return a.offsets ? std::min((int64_t)a.R, (int64_t)a.E + a.R / rows) : (a.R + rows - 1) / rows;
+}
+
 constexpr size_t kSmemMax = 227 * 1024;
 
 template <int NT, typename Y>
 cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     using S = Stream<NT>;
-    // tiles: at most this many (which experts have rows is known on the device only)
-    const int64_t row_tiles = a.offsets ? std::min((int64_t)a.R, (int64_t)a.E + a.R / NT) : (a.R + NT - 1) / NT;
-    const int64_t tiles = row_tiles * a.nb;
+    const int64_t tiles = row_tiles(a, NT) * a.nb;
     // K is split over a cluster while the CTAs still fit on the machine at once, every CTA
     // keeps two blocks of k or more, and each takes whole columns of the joined sums
     a.split = 1;
@@ -692,16 +725,14 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
 }
 
-template <int BN, typename Y>
+template <bool PAIR, typename Y>
 cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
-    using W = Wide<BN>;
-    const int64_t row_tiles = a.offsets ? std::min((int64_t)a.R, (int64_t)a.E + a.R / kWideRows)
-                                        : (a.R + kWideRows - 1) / kWideRows;
-    const int64_t tiles = row_tiles * ((a.N + BN - 1) / BN);
+    using W = Wide<PAIR>;
+    const int64_t tiles = row_tiles(a, W::kRows) * ((a.N + kWideCols - 1) / kWideCols);
     CUtensorMap tmx, tmw;
-    if (!encode_codes_map(&tmx, x, a.R, K, 128) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, BN / 2))
+    if (!encode_codes_map(&tmx, x, a.R, K, 128) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, W::kOwnCols))
         return cudaErrorInvalidValue;
-    auto kern = fp8_wide<BN, Y>;
+    auto kern = fp8_wide<PAIR, Y>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     if (e != cudaSuccess) return e;
     // the register split assumes the block launches at exactly kWideRegs a thread; any other
@@ -710,19 +741,47 @@ cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, in
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kWideRegs) return cudaErrorInvalidConfiguration;
-    const unsigned pairs = (unsigned)std::min<int64_t>(tiles, sms / 2);
-    kern<<<2 * pairs, kWideThreads, W::smem(a.E), st>>>(a, tmx, tmw);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(W::kCtas * std::min<int64_t>(tiles, sms / W::kCtas)));
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = W::smem(a.E);
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = W::kCtas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
 }
 
 template <typename Y>
 cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
-    // rows of a tile: the rows an expert has on average, doubled because experts differ
-    const int64_t typical = a.offsets ? std::min((int64_t)a.R, 2 * (((int64_t)a.R + a.E - 1) / a.E)) : a.R;
-    if (typical <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
-    if (typical <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
-    if (typical <= (a.offsets ? 96 : 64)) return launch_stream<64, Y>(a, x, w, K, sms, st);
-    return launch_wide<256, Y>(a, x, w, K, sms, st);
+    const int64_t cols = (a.N + kWideCols - 1) / kWideCols;
+    if (a.offsets) {
+        // Up to 32 rows: fp8_stream (64 experts of 1408 x 2048, 8 rows: 10.5 us, fp8_wide 11.8;
+        // 32 rows: 16.6, 18.4; but 64 rows: 33.4, 28.8). From 512 rows an expert on, pairs
+        // (64 experts, 32768 rows: 138 us, single CTAs 149; 16384 rows: 90 and 92, and below
+        // that single CTAs are ahead, whose row tiles are half as high: 4096 rows 60, 45).
+        if (a.R <= 32) return launch_stream<16, Y>(a, x, w, K, sms, st);
+        if (a.R >= 512 * (int64_t)a.E) return launch_wide<true, Y>(a, x, w, K, sms, st);
+        return launch_wide<false, Y>(a, x, w, K, sms, st);
+    }
+    // Few rows: fp8_stream while its tiles are done in one round, or in fewer half-width ones
+    // than fp8_wide's (11008 x 4096, 16 rows: 16.0 us, fp8_wide 18.5; 28672 x 8192, two rounds
+    // against one: 51 and 45; 14336 x 4096, 128 rows: 29.1 and 19.4)
+    const int64_t rounds = ((a.R + 63) / 64 * a.nb + sms - 1) / sms;
+    if (rounds == 1 || (a.R <= 64 && rounds < 2 * ((cols + sms - 1) / sms))) {
+        if (a.R <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
+        if (a.R <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
+        return launch_stream<64, Y>(a, x, w, K, sms, st);
+    }
+    // Pairs unless single CTAs are done in fewer rounds (333 x 11008 x 4096: two rounds of pairs
+    // 36.4 us, one of single CTAs 20.4; where both take as many, pairs are 2 to 5 % ahead)
+    const int64_t pairs = (row_tiles(a, 256) * cols + sms / 2 - 1) / (sms / 2);
+    const int64_t singles = (row_tiles(a, 128) * cols + sms - 1) / sms;
+    if (singles < pairs) return launch_wide<false, Y>(a, x, w, K, sms, st);
+    return launch_wide<true, Y>(a, x, w, K, sms, st);
 }
 
 int device_sms() {
