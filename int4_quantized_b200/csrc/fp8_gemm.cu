@@ -16,20 +16,22 @@
 //   warp 2      the rows' scales of each block, by 4-byte asynchronous copies
 //   warps 4-..  promotion and stores; lane = weight row, so stores of y are contiguous
 //
-// Many rows (fp8_wide): one CTA makes a tile of 128 rows of x x 256 weight rows, or a pair of
-// CTAs (cta_group::2) one of 256 x 256. In a pair each CTA loads its own rows of x and half of
-// the weights, so that a block of k costs an SM 32 KB from L2 instead of 48; single CTAs leave
-// fewer rows of a tile empty. Here D's lanes are rows of x, so that the scale of a thread's
+// Many rows (fp8_wide): one CTA makes a tile of 128 rows of x x 256 or 128 weight rows, or a
+// pair of CTAs (cta_group::2) one of 256 x 256. In a pair each CTA loads its own rows of x and
+// half of the weights, so that a block of k costs an SM 32 KB from L2 instead of 48 (which
+// single CTAs take at 60 bytes a clock, about all that an SM can); the smaller tiles leave
+// fewer rows empty and fill the machine sooner. Here D's lanes are rows of x, so that the scale of a thread's
 // whole row of D is one number a block of k.
 //   warp 0      TMA producer (of a pair both; all bytes are counted on the first CTA's barriers)
 //   warp 1      tensor memory; MMA issue (in the first CTA, for both)
-//   warps 4-11  promotion and stores: 32 rows x 128 columns a warp, kept in registers; the
+//   warps 4-11  promotion and stores: 32 rows x half of the columns a warp, kept in registers; the
 //               first four warps give theirs up to them (setmaxnreg)
 // Every wait is bounded (about one second); one that gives up sets Q4_STATUS_TIMEOUT in the
 // status word, and the roles run to completion without further waits.
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -422,7 +424,6 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
 }
 
 // ---- many rows ----------------------------------------------------------------------------
-constexpr int kWideCols = 256;     // weight rows a tile
 constexpr int kWideThreads = 384;  // TMA, MMA, two without a role, eight epilogue warps
 // The block launches with 168 registers a thread; the first warpgroup keeps 72, the two
 // epilogue warpgroups (128 fp32 sums a thread) take 216: 128 * 72 + 256 * 216 is exactly the
@@ -430,16 +431,17 @@ constexpr int kWideThreads = 384;  // TMA, MMA, two without a role, eight epilog
 constexpr int kWideRegs = 168, kWideLow = 72, kWideHigh = 216;
 static_assert(128 * kWideLow + 256 * kWideHigh == kWideThreads * kWideRegs, "register split");
 
-template <bool PAIR>
+// A tile of BN weight rows, made by one CTA or a pair.
+template <bool PAIR, int BN>
 struct Wide {
     static constexpr int kCtas = PAIR ? 2 : 1;
     static constexpr int kRows = 128 * kCtas;        // rows of x a tile
-    static constexpr int kOwnCols = kWideCols / kCtas;  // weight rows that a CTA loads
+    static constexpr int kOwnCols = BN / kCtas;  // weight rows that a CTA loads
     static constexpr int kXBytes = 128 * kBK;
     static constexpr int kStage = kXBytes + kOwnCols * kBK;
-    static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 4 of 48 KB
-    static constexpr int kBufs = 512 / kWideCols;    // all 512 columns of tensor memory
-    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kWideCols >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 4 of 48
+    static constexpr int kBufs = 512 / BN;    // all 512 columns of tensor memory
+    static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
     static size_t smem(int E) {
         return 1024 + (size_t)kStages * kStage + (2 * kStages + 2 * kBufs + 1) * 8 + 16 + (size_t)(2 * E + 2) * 4;
     }
@@ -473,11 +475,11 @@ Q4_DEVINL uint32_t two(float lo, float hi) {
     }
 }
 
-template <bool PAIR, typename Y>
+template <bool PAIR, int BN, typename Y>
 __global__ void __launch_bounds__(kWideThreads, 1)
 fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw) {
-    using W = Wide<PAIR>;
-    constexpr int HALF = kWideCols / 2;  // columns an epilogue warp keeps
+    using W = Wide<PAIR, BN>;
+    constexpr int HALF = BN / 2;  // columns an epilogue warp keeps
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + W::kStages * W::kStage);
@@ -523,7 +525,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
     if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int cols = (int)((a.N + kWideCols - 1) / kWideCols);
+    const int cols = (int)((a.N + BN - 1) / BN);
     const int64_t tiles = (int64_t)first[a.E] * cols, step = gridDim.x / W::kCtas, tile0 = blockIdx.x / W::kCtas;
     bool timed_out = false;
 
@@ -535,7 +537,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                 int filled = 0;
                 for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
                     const Tile t = tile_at(a, W::kRows, cols, first, rows0, j);
-                    const int wrow = (int)(t.e * a.N + (int64_t)t.nb * kWideCols + rank * W::kOwnCols);
+                    const int wrow = (int)(t.e * a.N + (int64_t)t.nb * BN + rank * W::kOwnCols);
                     const int xrow = t.row0 + rank * 128;
                     for (int kb = 0; kb < a.kb; ++kb) {
                         timed_out = !mbar_wait(empty + s.i, s.round ^ 1);
@@ -576,7 +578,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)
-                            umma_f8_of<PAIR>(dt + (uint32_t)(d.i * kWideCols), xd + 2 * kk, wd + 2 * kk, W::kIdesc,
+                            umma_f8_of<PAIR>(dt + (uint32_t)(d.i * BN), xd + 2 * kk, wd + 2 * kk, W::kIdesc,
                                              kk > 0 ? 1u : 0u);
                         umma_commit_of<PAIR>(empty + s.i);
                         umma_commit_of<PAIR>(dfull + d.i);
@@ -602,7 +604,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             const Tile t = tile_at(a, W::kRows, cols, first, rows0, j);
             const int rl = rank * 128 + 32 * q + lane;  // row inside the tile
             const bool live = rl < t.rows;
-            const int64_t n0 = (int64_t)t.nb * kWideCols + half * HALF;
+            const int64_t n0 = (int64_t)t.nb * BN + half * HALF;
             const float *xsc = a.xs + (int64_t)(t.row0 + min(rl, t.rows - 1)) * a.kb;
             const float *wsc = a.ws + ((int64_t)t.e * a.nb + min((int)(n0 / 128), a.nb - 1)) * a.kb;
             uint64_t acc[HALF / 2];
@@ -619,8 +621,8 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32) {
                     uint32_t v0[16], v1[16];
-                    tmem_ld16(lane_base + (uint32_t)(d.i * kWideCols + c), v0);
-                    tmem_ld16(lane_base + (uint32_t)(d.i * kWideCols + c + 16), v1);
+                    tmem_ld16(lane_base + (uint32_t)(d.i * BN + c), v0);
+                    tmem_ld16(lane_base + (uint32_t)(d.i * BN + c + 16), v1);
                     tmem_wait_ld();
                     if (c + 32 == HALF) {  // all read: the buffer is free
                         tc_fence_before();
@@ -693,6 +695,20 @@ int64_t row_tiles(const Fp8Args &a, int rows) {
 
 constexpr size_t kSmemMax = 227 * 1024;
 
+// Runs set() the first time on each device (a bit of `ready` each; every time beyond the 64th).
+// Two threads may both run it, with the same result.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> &ready, F set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <int NT, typename Y>
 cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     using S = Stream<NT>;
@@ -709,7 +725,10 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     if (!encode_codes_map(&tmx, x, a.R, K, NT) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, kWRows))
         return cudaErrorInvalidValue;
     auto kern = fp8_stream<NT, Y>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [&]() {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : (tiles < sms ? tiles : sms)));
@@ -725,22 +744,25 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
 }
 
-template <bool PAIR, typename Y>
+template <bool PAIR, int BN, typename Y>
 cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
-    using W = Wide<PAIR>;
-    const int64_t tiles = row_tiles(a, W::kRows) * ((a.N + kWideCols - 1) / kWideCols);
+    using W = Wide<PAIR, BN>;
+    const int64_t tiles = row_tiles(a, W::kRows) * ((a.N + BN - 1) / BN);
     CUtensorMap tmx, tmw;
     if (!encode_codes_map(&tmx, x, a.R, K, 128) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, W::kOwnCols))
         return cudaErrorInvalidValue;
-    auto kern = fp8_wide<PAIR, Y>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    auto kern = fp8_wide<PAIR, BN, Y>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [&]() -> cudaError_t {
+        // the register split assumes the block launches at exactly kWideRegs a thread; any other
+        // allocation could leave an increase waiting: refuse to launch
+        cudaFuncAttributes fa;
+        const cudaError_t ge = cudaFuncGetAttributes(&fa, kern);
+        if (ge != cudaSuccess) return ge;
+        if (fa.numRegs != kWideRegs) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    });
     if (e != cudaSuccess) return e;
-    // the register split assumes the block launches at exactly kWideRegs a thread; any other
-    // allocation could leave an increase waiting: refuse to launch
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kWideRegs) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(W::kCtas * std::min<int64_t>(tiles, sms / W::kCtas)));
     cfg.blockDim = dim3(kWideThreads);
@@ -757,31 +779,42 @@ cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, in
 
 template <typename Y>
 cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
-    const int64_t cols = (a.N + kWideCols - 1) / kWideCols;
     if (a.offsets) {
         // Up to 32 rows: fp8_stream (64 experts of 1408 x 2048, 8 rows: 10.5 us, fp8_wide 11.8;
-        // 32 rows: 16.6, 18.4; but 64 rows: 33.4, 28.8). From 512 rows an expert on, pairs
-        // (64 experts, 32768 rows: 138 us, single CTAs 149; 16384 rows: 90 and 92, and below
-        // that single CTAs are ahead, whose row tiles are half as high: 4096 rows 60, 45).
+        // 32 rows: 16.6, 18.4; but 64 rows: 33.4, 28.8)
         if (a.R <= 32) return launch_stream<16, Y>(a, x, w, K, sms, st);
-        if (a.R >= 512 * (int64_t)a.E) return launch_wide<true, Y>(a, x, w, K, sms, st);
-        return launch_wide<false, Y>(a, x, w, K, sms, st);
+    } else {
+        // Few rows: fp8_stream where its tiles leave SMs to split K over (11008 x 4096, 16 rows:
+        // 16.0 us, fp8_wide 18.5; 4096 x 11008, 128 rows: 26.0 and 33.9; but 4096 x 4096, 200
+        // rows: 18.0 and 16.8), and up to 64 rows where its rounds are no longer than fp8_wide's
+        // (28672 x 8192, two against one twice as wide: 51 and 45)
+        const int64_t tiles = (a.R + 63) / 64 * a.nb;
+        if (tiles * 2 <= sms ||
+            (a.R <= 64 && (tiles + sms - 1) / sms < 2 * (((a.N + 255) / 256 + sms - 1) / sms))) {
+            if (a.R <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
+            if (a.R <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
+            return launch_stream<64, Y>(a, x, w, K, sms, st);
+        }
     }
-    // Few rows: fp8_stream while its tiles are done in one round, or in fewer half-width ones
-    // than fp8_wide's (11008 x 4096, 16 rows: 16.0 us, fp8_wide 18.5; 28672 x 8192, two rounds
-    // against one: 51 and 45; 14336 x 4096, 128 rows: 29.1 and 19.4)
-    const int64_t rounds = ((a.R + 63) / 64 * a.nb + sms - 1) / sms;
-    if (rounds == 1 || (a.R <= 64 && rounds < 2 * ((cols + sms - 1) / sms))) {
-        if (a.R <= 16) return launch_stream<16, Y>(a, x, w, K, sms, st);
-        if (a.R <= 32) return launch_stream<32, Y>(a, x, w, K, sms, st);
-        return launch_stream<64, Y>(a, x, w, K, sms, st);
-    }
-    // Pairs unless single CTAs are done in fewer rounds (333 x 11008 x 4096: two rounds of pairs
-    // 36.4 us, one of single CTAs 20.4; where both take as many, pairs are 2 to 5 % ahead)
-    const int64_t pairs = (row_tiles(a, 256) * cols + sms / 2 - 1) / (sms / 2);
-    const int64_t singles = (row_tiles(a, 128) * cols + sms - 1) / sms;
-    if (singles < pairs) return launch_wide<false, Y>(a, x, w, K, sms, st);
-    return launch_wide<true, Y>(a, x, w, K, sms, st);
+    // The shape of fp8_wide's tiles by the rounds they take: a round of 256 x 256 by pairs, of
+    // 128 x 256 and of 128 x 128 by single CTAs takes times as 19 : 20 : 15 (4096 x 4096, 512
+    // rows, one round of each: 20.1, 21.1 and 17.4 us; 11008 x 4096, 333 rows, 2, 1 and 2 rounds:
+    // 36.4, 21.2 and 29.7).
+    auto rounds = [&](int rows, int width, int64_t at_once) {
+        // row tiles: experts with less than half a tile of rows have one each, others on average
+        // half a tile more than their rows fill
+        const int64_t E = a.offsets ? a.E : 1, R = a.R;
+        const int64_t rt = !a.offsets ? (R + rows - 1) / rows : R * 2 < E * rows ? std::min(R, E) : R / rows + (E + 1) / 2;
+        return (rt * ((a.N + width - 1) / width) + at_once - 1) / at_once;
+    };
+    const int64_t pair = 19 * rounds(256, 256, sms / 2), single = 20 * rounds(128, 256, sms),
+                  narrow = 15 * rounds(128, 128, sms);
+    // (64 experts of 1408 x 2048 with 512 rows each: pairs 138 us, single CTAs 149, at 13 and 12
+    // rounds: many rounds together are slower by what they ask of L2)
+    if (a.offsets ? a.R >= 512 * (int64_t)a.E : pair <= single && pair <= narrow)
+        return launch_wide<true, 256, Y>(a, x, w, K, sms, st);
+    if (narrow < single) return launch_wide<false, 128, Y>(a, x, w, K, sms, st);
+    return launch_wide<false, 256, Y>(a, x, w, K, sms, st);
 }
 
 int device_sms() {
