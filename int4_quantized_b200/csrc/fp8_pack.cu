@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "unaligned.cuh"
 
 namespace q4 {
 
@@ -25,9 +26,6 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr uint32_t kInf = 0x7f800000u;
 
-Q4_DEVINL float to_f32(float v) { return v; }
-Q4_DEVINL float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-Q4_DEVINL float to_f32(__half v) { return __half2float(v); }
 
 // 16 bytes of T as fp32 values (NEG: negated).
 template <typename T, bool NEG>
@@ -59,39 +57,30 @@ Q4_DEVINL void ld_v8(const void *p, uint4 &a, uint4 &b) {
 // N consecutive values of a row, of which `left` (which may be negative) are inside it; zeros
 // behind. The loads and their conversion are apart, so that a thread has all of its loads on
 // their way before it waits for the first. NEG gives the values negated.
+// VEC: a row's values are whole chunks of N at 32-byte addresses (16-byte ones for a chunk of
+// 16 bytes); else rows begin anywhere and end anywhere.
 template <typename T, int N, bool VEC>
 struct Chunk {
-    static constexpr int PER = 16 / (int)sizeof(T);
-    typename std::conditional<VEC, uint4, T>::type raw[VEC ? N / PER : N];
+    static constexpr int PER = 16 / (int)sizeof(T), WORDS = N / PER;
+    uint4 raw[WORDS];
     Q4_DEVINL void load(const T *p, int left) {
-        if constexpr (VEC) {  // a row's values are whole chunks of N here
+        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < N / PER; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < WORDS; ++i) raw[i] = make_uint4(0, 0, 0, 0);
             if (left > 0) {
-                if constexpr (N / PER == 1) {
-                    raw[0] = *reinterpret_cast<const uint4 *>(p);
-                } else {
 #pragma unroll
-                    for (int i = 0; i < N / PER; i += 2) ld_v8(p + i * PER, raw[i], raw[i + 1]);
-                }
+                for (int i = 0; i < WORDS; i += 2) ld_v8(p + i * PER, raw[i], raw[i + 1]);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                raw[i] = T(0.f);
-                if (i < left) raw[i] = p[i];
-            }
+            for (int i = 0; i < WORDS; ++i)
+                raw[i] = load_any16(p + i * PER, max(0, min(left - i * PER, PER)) * (int)sizeof(T));
         }
     }
     template <bool NEG>
     Q4_DEVINL void values(float (&v)[N]) const {
-        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < N / PER; ++i) unpack16<T, NEG>(raw[i], v + i * PER);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = NEG ? -to_f32(raw[i]) : to_f32(raw[i]);
-        }
+        for (int i = 0; i < WORDS; ++i) unpack16<T, NEG>(raw[i], v + i * PER);
     }
 };
 
@@ -297,9 +286,7 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
         if constexpr (VEC) {
             if (left[j] > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
         } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i < left[j]) p[i] = (uint8_t)(c[i / 4] >> (8 * (i & 3)));
+            store_any16(p, make_uint4(c[0], c[1], c[2], c[3]), left[j]);
         }
         if (sub == j) {
             a.scales[(int64_t)row[j] * a.kb + blk[j]] = d.s;
@@ -354,17 +341,22 @@ __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__res
         uint32_t c[PER / 4];
         codes_of<PER>(nv, d, c);
         uint8_t *p = dst + n * K + k0;
+        uint4 out = make_uint4(c[0], c[1], 0, 0);
+        if constexpr (PER == 16) out.z = c[2], out.w = c[3];
         if constexpr (VEC) {
             if (k0 < K) {
-                if constexpr (PER == 16)
-                    *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
-                else
-                    *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
+                if constexpr (PER == 16) *reinterpret_cast<uint4 *>(p) = out;
+                else *reinterpret_cast<uint2 *>(p) = make_uint2(out.x, out.y);
             }
         } else {
+            const int left = (int)min(K - k0, (int64_t)PER);
+            if constexpr (PER == 16) {
+                store_any16(p, out, left);
+            } else {
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (k0 + j < K) p[j] = (uint8_t)(c[j / 4] >> (8 * (j & 3)));
+                for (int j = 0; j < PER; ++j)
+                    if (j < left) p[j] = (uint8_t)(c[j / 4] >> (8 * (j & 3)));
+            }
         }
     }
     if (threadIdx.x == 0) {

@@ -173,30 +173,30 @@ __global__ void __launch_bounds__(32 * kSortWarps) moe_sort_kernel(const T *__re
 }
 
 // ---- rows ---------------------------------------------------------------------------------
-// VEC: 16 bytes an access; else one element of T.
-template <typename T, bool VEC>
+// Rows of T in accesses of B bytes: 16 where rows are whole such parts at 16-byte addresses,
+// else 4 or an element. (Aligned 16-byte accesses shifted to unaligned rows took longer than
+// single elements: 8192 tokens x 4 of 4097 bf16 values, combine 215 us and 131.)
+template <typename T, int B>
 struct Row {
-    using V = typename std::conditional<VEC, uint4, T>::type;
-    static constexpr int N = VEC ? 16 / (int)sizeof(T) : 1;
+    using V = typename std::conditional<B == 16, uint4, typename std::conditional<B == 4, uint32_t, uint16_t>::type>::type;
+    static constexpr int N = B / (int)sizeof(T);
 };
-template <typename T, bool VEC>
-Q4_DEVINL void unpack(const typename Row<T, VEC>::V &r, float (&f)[Row<T, VEC>::N]) {
-    constexpr int N = Row<T, VEC>::N;
+template <typename T, int B>
+Q4_DEVINL void unpack(const typename Row<T, B>::V &r, float (&f)[Row<T, B>::N]) {
     const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < Row<T, B>::N; ++i) {
         if constexpr (std::is_same<T, float>::value) f[i] = e[i];
         else if constexpr (std::is_same<T, __half>::value) f[i] = __half2float(e[i]);
         else f[i] = __bfloat162float(e[i]);
     }
 }
-template <typename T, bool VEC>
-Q4_DEVINL typename Row<T, VEC>::V pack(const float (&f)[Row<T, VEC>::N]) {
-    constexpr int N = Row<T, VEC>::N;
-    typename Row<T, VEC>::V r;
+template <typename T, int B>
+Q4_DEVINL typename Row<T, B>::V pack(const float (&f)[Row<T, B>::N]) {
+    typename Row<T, B>::V r;
     T *e = reinterpret_cast<T *>(&r);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < Row<T, B>::N; ++i) {
         if constexpr (std::is_same<T, float>::value) e[i] = f[i];
         else if constexpr (std::is_same<T, __half>::value) e[i] = __float2half_rn(f[i]);
         else e[i] = __float2bfloat16_rn(f[i]);
@@ -204,13 +204,17 @@ Q4_DEVINL typename Row<T, VEC>::V pack(const float (&f)[Row<T, VEC>::N]) {
     return r;
 }
 
-constexpr int kInFlight = 8;  // accesses a lane
+// Accesses a lane has on its way: the narrower, the more.
+template <int B>
+constexpr int kInFlight = B == 16 ? 8 : 16;
 
 // Rows written once: they go first when L2 is full, so that x, which each expert reads again,
-// stays (8192 tokens x 8 of 4096 bf16 values: 132 us without, 122 with).
+// stays (8192 tokens x 8 of 4096 bf16 values: 132 us without, 122 with; the writes alone take
+// 74). Narrower accesses leave a sector to the next store, so theirs stay too.
 template <typename V>
 Q4_DEVINL void store_once(V *p, V v) {
-    __stcs(p, v);
+    if constexpr (sizeof(V) == 16) __stcs(p, v);
+    else *p = v;
 }
 
 // A warp copies P parts of 32 accesses from each of kInFlight / P rows.
@@ -218,7 +222,7 @@ template <typename V, int P>
 __global__ void __launch_bounds__(256) moe_gather_kernel(const V *__restrict__ x, int64_t T,
                                                          const int32_t *__restrict__ tokens, int64_t R, int64_t per_row,
                                                          uint32_t chunks, V *__restrict__ xs) {
-    constexpr int ROWS = kInFlight / P;
+    constexpr int ROWS = kInFlight<(int)sizeof(V)> / P;
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t g = unit / chunks, ch = unit - g * chunks;
     const int64_t v0 = (int64_t)ch * (32 * P) + (threadIdx.x & 31);
@@ -244,14 +248,14 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const V *__restrict__ x
 }
 
 // A warp sums P parts of 32 accesses of a row, S slots at a time.
-template <typename T, bool VEC, int S, int P>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, VEC>::V *__restrict__ ys, int64_t R,
+template <typename T, int B, int S, int P>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, B>::V *__restrict__ ys, int64_t R,
                                                           const int32_t *__restrict__ pos,
                                                           const float *__restrict__ weights, int64_t tokens, int k,
                                                           int64_t per_row, uint32_t chunks,
-                                                          typename Row<T, VEC>::V *__restrict__ out) {
-    using V = typename Row<T, VEC>::V;
-    constexpr int N = Row<T, VEC>::N;
+                                                          typename Row<T, B>::V *__restrict__ out) {
+    using V = typename Row<T, B>::V;
+    constexpr int N = Row<T, B>::N;
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t t = unit / chunks, ch = unit - t * chunks;
     if (t >= tokens) return;
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, 
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 float f[N];
-                unpack<T, VEC>(r[j][i], f);
+                unpack<T, B>(r[j][i], f);
 #pragma unroll
                 for (int n = 0; n < N; ++n) acc[i][n] = fmaf(w[j], f[n], acc[i][n]);
             }
@@ -289,19 +293,19 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, 
     }
 #pragma unroll
     for (int i = 0; i < P; ++i)
-        if (v0 + 32 * i < per_row) out[(int64_t)t * per_row + v0 + 32 * i] = pack<T, VEC>(acc[i]);
+        if (v0 + 32 * i < per_row) out[(int64_t)t * per_row + v0 + 32 * i] = pack<T, B>(acc[i]);
 }
 
 // W warps take one token, S slots at a time and P accesses of each; 4 / W tokens a CTA.
-template <typename T, bool VEC, int W, int S, int P>
-__global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, VEC>::V *__restrict__ dout,
-                                                       const typename Row<T, VEC>::V *__restrict__ ys, int64_t R,
+template <typename T, int B, int W, int S, int P>
+__global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, B>::V *__restrict__ dout,
+                                                       const typename Row<T, B>::V *__restrict__ ys, int64_t R,
                                                        const int32_t *__restrict__ pos,
                                                        const float *__restrict__ weights, int64_t tokens, int k,
-                                                       int64_t per_row, typename Row<T, VEC>::V *__restrict__ dys,
+                                                       int64_t per_row, typename Row<T, B>::V *__restrict__ dys,
                                                        float *__restrict__ dweights) {
-    using V = typename Row<T, VEC>::V;
-    constexpr int N = Row<T, VEC>::N;
+    using V = typename Row<T, B>::V;
+    constexpr int N = Row<T, B>::N;
     __shared__ float part[4][S];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (4 / W) + warp / W, s0 = t * k;
@@ -334,18 +338,18 @@ __global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, VEC
                 const int64_t v = v0 + 32 * W * i;
                 if (v >= per_row) break;
                 float g[N];
-                unpack<T, VEC>(g0[i], g);
+                unpack<T, B>(g0[i], g);
 #pragma unroll
                 for (int j = 0; j < S; ++j) {
                     if (p[j] < 0) continue;
                     float f[N], d[N];
-                    unpack<T, VEC>(r[j][i], f);
+                    unpack<T, B>(r[j][i], f);
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
                         dot[j] = fmaf(g[n], f[n], dot[j]);
                         d[n] = w[j] * g[n];
                     }
-                    dys[(int64_t)p[j] * per_row + v] = pack<T, VEC>(d);
+                    dys[(int64_t)p[j] * per_row + v] = pack<T, B>(d);
                 }
             }
         }
@@ -368,9 +372,7 @@ __global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, VEC
     }
 }
 
-inline int elem_size(q4_dtype t) { return t == Q4_F32 ? 4 : 2; }
 inline bool dtype_ok(q4_dtype t) { return t == Q4_F32 || t == Q4_BF16 || t == Q4_F16; }
-inline bool aligned16(const void *p) { return (uintptr_t)p % 16 == 0; }
 
 // Warps of a launch over rows x chunks, eight a CTA; 0 where the grid cannot hold them.
 inline unsigned row_grid(int64_t rows, int64_t chunks) {
@@ -413,11 +415,19 @@ inline int row_parts(int64_t per_row, int most) {
     return p;
 }
 
+// Bytes of an access to rows of D elements of `size` bytes at these addresses.
+inline int access_bytes(int64_t D, int size, const void *a, const void *b, const void *c = nullptr) {
+    const uintptr_t all = (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uintptr_t)(D * size);
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : size;
+}
+
 template <typename V>
-cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64_t R, int64_t per_row, void *xs,
+cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64_t R, int64_t bytes, void *xs,
                           cudaStream_t st, bool *fits) {
-    const int P = row_parts(per_row, kInFlight);
-    const int64_t chunks = (per_row + 32 * P - 1) / (32 * P), groups = (R + kInFlight / P - 1) / (kInFlight / P);
+    constexpr int F = kInFlight<(int)sizeof(V)>;
+    const int64_t per_row = bytes / (int64_t)sizeof(V);
+    const int P = row_parts(per_row, F);
+    const int64_t chunks = (per_row + 32 * P - 1) / (32 * P), groups = (R + F / P - 1) / (F / P);
     const unsigned grid = row_grid(groups, chunks);
     *fits = grid != 0;
     if (!grid) return cudaSuccess;
@@ -427,26 +437,32 @@ cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64
     if (P == 1) Q4_GATHER(1);
     else if (P == 2) Q4_GATHER(2);
     else if (P == 4) Q4_GATHER(4);
-    else Q4_GATHER(8);
+    else if (P == 8) Q4_GATHER(8);
+    else Q4_GATHER(F);
 #undef Q4_GATHER
     return cudaGetLastError();
 }
 
-template <typename T, bool VEC>
+template <typename T, int B>
 cudaError_t combine_rows(const void *ys, int64_t R, const int32_t *pos, const float *weights, int64_t tokens, int k,
-                         int64_t per_row, void *out, cudaStream_t st, bool *fits) {
-    using V = typename Row<T, VEC>::V;
-    // slots times parts of a row: eight accesses on their way where the row is long enough
-    const int P = row_parts(per_row, k == 1 ? 8 : k == 2 ? 4 : 2);
+                         int64_t D, void *out, cudaStream_t st, bool *fits) {
+    using V = typename Row<T, B>::V;
+    constexpr int M = kInFlight<B> / 8;
+    const int64_t per_row = D / Row<T, B>::N;
+    // slots times parts of a row: as many accesses on their way where the row is long enough
+    const int P = row_parts(per_row, M * (k == 1 ? 8 : k == 2 ? 4 : 2));
     const int64_t chunks = (per_row + 32 * P - 1) / (32 * P);
     const unsigned grid = row_grid(tokens, chunks);
     *fits = grid != 0;
     if (!grid) return cudaSuccess;
-#define Q4_COMBINE(S_, P_)                                                                                            \
-    moe_combine_kernel<T, VEC, S_, P_><<<grid, 256, 0, st>>>(static_cast<const V *>(ys), R, pos, weights, tokens, k, \
-                                                             per_row, (uint32_t)chunks, static_cast<V *>(out))
-    if (P == 8) Q4_COMBINE(1, 8);
-    else if (P == 4) Q4_COMBINE(2, 4);
+#define Q4_COMBINE(S_, P_)                                                                                          \
+    moe_combine_kernel<T, B, S_, P_><<<grid, 256, 0, st>>>(static_cast<const V *>(ys), R, pos, weights, tokens, k, \
+                                                           per_row, (uint32_t)chunks, static_cast<V *>(out))
+    if (P == 16) Q4_COMBINE(1, 16);
+    else if (P == 8 && k == 1) Q4_COMBINE(1, 8);
+    else if (P == 8) Q4_COMBINE(2, 8);
+    else if (P == 4 && k <= 2) Q4_COMBINE(2, 4);
+    else if (P == 4) Q4_COMBINE(4, 4);
     else if (P == 2) Q4_COMBINE(4, 2);
     else Q4_COMBINE(8, 1);
 #undef Q4_COMBINE
@@ -456,25 +472,27 @@ cudaError_t combine_rows(const void *ys, int64_t R, const int32_t *pos, const fl
 template <typename T>
 cudaError_t combine_launch(const void *ys, int64_t R, const int32_t *pos, const float *weights, int64_t tokens, int k,
                            int64_t D, void *out, cudaStream_t st, bool *fits) {
-    const int64_t bytes = D * (int64_t)sizeof(T);
-    if (bytes % 16 == 0 && aligned16(ys) && aligned16(out))
-        return combine_rows<T, true>(ys, R, pos, weights, tokens, k, bytes / 16, out, st, fits);
-    return combine_rows<T, false>(ys, R, pos, weights, tokens, k, D, out, st, fits);
+    const int B = access_bytes(D, sizeof(T), ys, out);
+    if (B == 16) return combine_rows<T, 16>(ys, R, pos, weights, tokens, k, D, out, st, fits);
+    if (B == 4) return combine_rows<T, 4>(ys, R, pos, weights, tokens, k, D, out, st, fits);
+    return combine_rows<T, sizeof(T)>(ys, R, pos, weights, tokens, k, D, out, st, fits);
 }
 
-template <typename T, bool VEC>
+template <typename T, int B>
 cudaError_t bwd_rows(const void *dout, const void *ys, int64_t R, const int32_t *pos, const float *weights,
-                     int64_t tokens, int k, int64_t per_row, void *dys, float *dweights, cudaStream_t st) {
-    using V = typename Row<T, VEC>::V;
-#define Q4_BWD(W_, S_, P_)                                                                                             \
-    moe_combine_bwd<T, VEC, W_, S_, P_><<<(unsigned)((tokens + 4 / W_ - 1) / (4 / W_)), 128, 0, st>>>(                 \
-        static_cast<const V *>(dout), static_cast<const V *>(ys), R, pos, weights, tokens, k, per_row,                 \
+                     int64_t tokens, int k, int64_t D, void *dys, float *dweights, cudaStream_t st) {
+    using V = typename Row<T, B>::V;
+    const int64_t per_row = D / Row<T, B>::N;
+#define Q4_BWD(W_, S_, P_)                                                                                           \
+    moe_combine_bwd<T, B, W_, S_, P_><<<(unsigned)((tokens + 4 / W_ - 1) / (4 / W_)), 128, 0, st>>>(                 \
+        static_cast<const V *>(dout), static_cast<const V *>(ys), R, pos, weights, tokens, k, per_row,               \
         static_cast<V *>(dys), dweights)
     // rows below 128 accesses leave three of four warps idle: one warp a token there
-    // (65536 tokens x 8 of 256 bf16 values: 290 us with four)
+    // (65536 tokens x 8 of 256 bf16 values: 290 us with four, 129 with one)
+    constexpr int M = B == 16 ? 1 : 4;
     if (per_row >= 128) {
-        if (k <= 2) Q4_BWD(4, 2, 4);
-        else Q4_BWD(4, 8, 1);
+        if (k <= 2) Q4_BWD(4, 2, 4 * M);
+        else Q4_BWD(4, 8, M);
     } else {
         if (k <= 2) Q4_BWD(1, 2, 2);
         else Q4_BWD(1, 8, 1);
@@ -486,10 +504,10 @@ cudaError_t bwd_rows(const void *dout, const void *ys, int64_t R, const int32_t 
 template <typename T>
 cudaError_t bwd_launch(const void *dout, const void *ys, int64_t R, const int32_t *pos, const float *weights,
                        int64_t tokens, int k, int64_t D, void *dys, float *dweights, cudaStream_t st) {
-    const int64_t bytes = D * (int64_t)sizeof(T);
-    if (bytes % 16 == 0 && aligned16(ys) && aligned16(dout) && aligned16(dys))
-        return bwd_rows<T, true>(dout, ys, R, pos, weights, tokens, k, bytes / 16, dys, dweights, st);
-    return bwd_rows<T, false>(dout, ys, R, pos, weights, tokens, k, D, dys, dweights, st);
+    const int B = access_bytes(D, sizeof(T), dout, ys, dys);
+    if (B == 16) return bwd_rows<T, 16>(dout, ys, R, pos, weights, tokens, k, D, dys, dweights, st);
+    if (B == 4) return bwd_rows<T, 4>(dout, ys, R, pos, weights, tokens, k, D, dys, dweights, st);
+    return bwd_rows<T, sizeof(T)>(dout, ys, R, pos, weights, tokens, k, D, dys, dweights, st);
 }
 
 // Shapes that every call below shares: slots and rows in 32 bits.
@@ -526,13 +544,12 @@ q4_status q4_moe_gather(const void *x, q4_dtype xt, int64_t T, int64_t D, const 
     if (s != Q4_OK) return s;
     if (R == 0 || T == 0) return Q4_OK;
     if (!x || !tokens || !xs) return Q4_ERR_ARG;
-    const int64_t bytes = D * q4::elem_size(xt);
+    const int size = xt == Q4_F32 ? 4 : 2, B = q4::access_bytes(D, size, x, xs);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     bool fits = true;
-    const cudaError_t e = bytes % 16 == 0 && q4::aligned16(x) && q4::aligned16(xs)
-                              ? q4::gather_launch<uint4>(x, T, tokens, R, bytes / 16, xs, st, &fits)
-                          : xt == Q4_F32 ? q4::gather_launch<uint32_t>(x, T, tokens, R, D, xs, st, &fits)
-                                         : q4::gather_launch<uint16_t>(x, T, tokens, R, D, xs, st, &fits);
+    const cudaError_t e = B == 16  ? q4::gather_launch<uint4>(x, T, tokens, R, D * size, xs, st, &fits)
+                          : B == 4 ? q4::gather_launch<uint32_t>(x, T, tokens, R, D * size, xs, st, &fits)
+                                   : q4::gather_launch<uint16_t>(x, T, tokens, R, D * size, xs, st, &fits);
     if (!fits) return Q4_ERR_UNSUPPORTED;
     return q4::cuda_error(e, "moe_gather launch");
 }

@@ -78,7 +78,7 @@ def test_sort_large(q4):
 
 
 # ---- gather and combine -----------------------------------------------------------------------
-ROWS = [("f32", 1), ("f32", 4), ("f32", 1023), ("bf16", 7), ("bf16", 64), ("bf16", 4096), ("f16", 258), ("f16", 2056)]
+ROWS = [("bf16", 1001), ("f16", 2057), ("f32", 1), ("f32", 4), ("f32", 1023), ("bf16", 7), ("bf16", 64), ("bf16", 4096), ("f16", 258), ("f16", 2056)]
 
 
 @pytest.mark.parametrize("x_type,D", ROWS)
