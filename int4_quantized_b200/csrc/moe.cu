@@ -207,6 +207,7 @@ Q4_DEVINL typename Row<T, B>::V pack(const float (&f)[Row<T, B>::N]) {
 // Accesses a lane has on its way: the narrower, the more.
 template <int B>
 constexpr int kInFlight = B == 16 ? 8 : 16;
+constexpr int kGatherInFlight = 8;  // (16 of an element: 8192 x 4 of 4097 bf16 values 182 us, 8: 114)
 
 // Rows written once: they go first when L2 is full, so that x, which each expert reads again,
 // stays (8192 tokens x 8 of 4096 bf16 values: 132 us without, 122 with; the writes alone take
@@ -222,7 +223,7 @@ template <typename V, int P>
 __global__ void __launch_bounds__(256) moe_gather_kernel(const V *__restrict__ x, int64_t T,
                                                          const int32_t *__restrict__ tokens, int64_t R, int64_t per_row,
                                                          uint32_t chunks, V *__restrict__ xs) {
-    constexpr int ROWS = kInFlight<(int)sizeof(V)> / P;
+    constexpr int ROWS = kGatherInFlight / P;
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t g = unit / chunks, ch = unit - g * chunks;
     const int64_t v0 = (int64_t)ch * (32 * P) + (threadIdx.x & 31);
@@ -424,7 +425,7 @@ inline int access_bytes(int64_t D, int size, const void *a, const void *b, const
 template <typename V>
 cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64_t R, int64_t bytes, void *xs,
                           cudaStream_t st, bool *fits) {
-    constexpr int F = kInFlight<(int)sizeof(V)>;
+    constexpr int F = kGatherInFlight;
     const int64_t per_row = bytes / (int64_t)sizeof(V);
     const int P = row_parts(per_row, F);
     const int64_t chunks = (per_row + 32 * P - 1) / (32 * P), groups = (R + F / P - 1) / (F / P);
@@ -437,8 +438,7 @@ cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64
     if (P == 1) Q4_GATHER(1);
     else if (P == 2) Q4_GATHER(2);
     else if (P == 4) Q4_GATHER(4);
-    else if (P == 8) Q4_GATHER(8);
-    else Q4_GATHER(F);
+    else Q4_GATHER(8);
 #undef Q4_GATHER
     return cudaGetLastError();
 }
