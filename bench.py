@@ -624,14 +624,100 @@ def qpack_section(args, dev, peaks):
 
 
 # ----------------------------------------------------------------------------------------
+FP8_CASES = {"fp8_pack": "M K", "fp8_pack_weights": "N K", "fp8_gemm": "N K M", "fp8_grouped": "E N K rows",
+             "moe": "E D k T", "experts": "E D F k T"}
+
+
+def run_fp8_case(a, dev, gen):
+    """One case of the 8-bit floating-point and routing calls (bf16 activations, inputs as many
+    copies as exceed twice the L2): microseconds, and bytes and operations over that time."""
+    import torch
+
+    import int4_quantized_b200 as q4
+
+    if len(a.shape) != len(FP8_CASES[a.kind].split()):
+        raise SystemExit(f"bench.py --case {a.kind} {FP8_CASES[a.kind]}")
+
+    def rows(*shape):
+        return torch.randn(*shape, device=dev, generator=gen).to(torch.bfloat16)
+
+    def routing(E, k, T):
+        top = torch.topk(torch.randn(T, E, device=dev, generator=gen), k, 1)
+        return top.indices, torch.softmax(top.values, 1)
+
+    def copies(nbytes, make):
+        return [make() for _ in range(_l2_copies(nbytes))]
+
+    flops = 0.0
+    if a.kind == "fp8_pack":
+        M, K = a.shape
+        nbytes = 3 * M * K + 4 * M * -(-K // 128)
+        X = copies(nbytes, lambda: rows(M, K))
+        out = q4.fp8_pack(X[0])
+        calls = {"fp8_pack": lambda i: q4.fp8_pack(X[i % len(X)], codes=out[0], scales=out[1])}
+    elif a.kind == "fp8_pack_weights":
+        N, K = a.shape
+        nbytes = 5 * N * K
+        X = copies(nbytes, lambda: torch.randn(N, K, device=dev, generator=gen) * 0.02)
+        out = q4.fp8_pack_weights(X[0])
+        calls = {"fp8_pack_weights": lambda i: q4.fp8_pack_weights(X[i % len(X)], codes=out[0], scales=out[1])}
+    elif a.kind == "fp8_gemm":
+        N, K, M = a.shape
+        nbytes, flops = N * K + M * (K + 2 * N), 2.0 * M * N * K
+        w = rows(N, K) * 0.02
+        X = copies(nbytes, lambda: (q4.fp8_pack(rows(M, K)), q4.fp8_pack_weights(w)))
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        calls = {"fp8_gemm": lambda i: q4.fp8_gemm(*X[i % len(X)][0], *X[i % len(X)][1], out=y)}
+    elif a.kind == "fp8_grouped":
+        E, N, K, R = a.shape
+        ids = torch.randint(0, E, (R, 1), device=dev, generator=gen)
+        _, _, off = q4.moe_sort(ids, E)
+        nbytes, flops = min(E, R) * N * K + R * (K + 2 * N), 2.0 * R * N * K
+        w = rows(E, N, K) * 0.02
+        X = copies(nbytes, lambda: (q4.fp8_pack(rows(R, K)), q4.fp8_pack_weights(w)))
+        y = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        calls = {"fp8_grouped": lambda i: q4.fp8_gemm_grouped(*X[i % len(X)][0], *X[i % len(X)][1], off, out=y)}
+    elif a.kind == "moe":
+        E, D, k, T = a.shape
+        ids, w = routing(E, k, T)
+        tokens, pos, _ = q4.moe_sort(ids, E)
+        nbytes = 2 * D * (T + T * k)
+        X = copies(nbytes, lambda: (rows(T, D), rows(T * k, D)))
+        xs, out, dys = rows(T * k, D), rows(T, D), rows(T * k, D)
+        calls = {"sort": lambda i: q4.moe_sort(ids, E),
+                 "gather": lambda i: q4.moe_gather(X[i % len(X)][0], tokens, out=xs),
+                 "combine": lambda i: q4.moe_combine(X[i % len(X)][1], pos, w, out=out),
+                 "combine_backward": lambda i: q4.moe_combine_backward(*X[i % len(X)], pos, w, dys=dys)}
+    else:
+        E, D, F, k, T = a.shape
+        ids, w = routing(E, k, T)
+        layer = q4.Fp8Experts.pack(rows(E, 2 * F, D) * 0.02, rows(E, D, F) * 0.02)
+        nbytes, flops = 3 * min(E, T * k) * D * F, 6.0 * T * k * D * F
+        X = [rows(T, D) for _ in range(4)]
+        calls = {"experts": lambda i: layer(X[i % 4], ids, w)}
+    ncopy = len(X)
+    for name, call in calls.items():
+        us, us_max = time_calls(call, ncopy, a.reps, a.warmup, a.batches)
+        line = {"kind": name, "shape": f"{FP8_CASES[a.kind]} = {' '.join(map(str, a.shape))}", "us_median": round(us, 3),
+                "us_max": round(us_max, 3), "copies": ncopy}
+        if name != "sort":
+            n = nbytes + (2 * a.shape[1] * a.shape[2] * a.shape[3] if name == "combine_backward" else 0)
+            line["GB/s"] = round(n / (us * 1e-6) / 1e9, 1)
+        if flops:
+            line["TFLOPs"] = round(flops / (us * 1e-6) / 1e12, 2)
+        print(json.dumps(line), flush=True)
+    return 0
+
+
 def run_case(argv):
     """One library call on a seeded shape, timed; the command line profilers are pointed at."""
     ap = argparse.ArgumentParser(prog="bench.py --case", description=(
-        "qgemm N K bits group [M] | qpack N K bits group | stack bits group. W ~ N(0, 0.02) and x ~ N(0, 1) "
+        "qgemm N K bits group [M] | qpack N K bits group | stack bits group | "
+        + " | ".join(f"{k} {v}" for k, v in FP8_CASES.items()) + ". W ~ N(0, 0.02) and x ~ N(0, 1) "
         "from a fixed device seed; inputs copied until they exceed twice the L2 (at most 64 copies); --reps "
         "calls captured in one CUDA graph and timed with CUDA events. The stack case is the Llama-7B-shaped "
         "decode step (group 0 = one scale per output channel)."))
-    ap.add_argument("kind", choices=["qgemm", "qpack", "stack"])
+    ap.add_argument("kind", choices=["qgemm", "qpack", "stack", *FP8_CASES])
     ap.add_argument("shape", type=int, nargs="+")
     ap.add_argument("--bf16", action="store_true", help="x in bfloat16 (qgemm)")
     ap.add_argument("--static", action="store_true", help="weights declared static (qgemm)")
@@ -646,6 +732,8 @@ def run_case(argv):
 
     dev = torch.device("cuda", torch.cuda.current_device())
     gen = torch.Generator(device=dev).manual_seed(0)
+    if a.kind in FP8_CASES:
+        return run_fp8_case(a, dev, gen)
     if a.kind == "stack":
         from int4_quantized_b200 import decode_stack as ds
 
