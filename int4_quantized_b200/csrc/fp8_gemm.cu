@@ -237,6 +237,7 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
         tmem_alloc(tmem_slot, S::kCols);
         tmem_relinquish();
     }
+    begin_overlapped();  // nothing above touches global memory
     count_tiles(a, NT, first, rows0);
     tc_fence_before();
     __syncthreads();
@@ -519,6 +520,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             tmem_relinquish();
         }
     }
+    begin_overlapped();  // nothing above touches global memory
     count_tiles(a, W::kRows, first, rows0);
     tc_fence_before();
     __syncthreads();
@@ -730,18 +732,8 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : (tiles < sms ? tiles : sms)));
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)a.split;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
+    const unsigned grid = (unsigned)(a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms));
+    return launch_overlapped(kern, grid, S::kThreads, smem, st, (unsigned)a.split, a, tmx, tmw);
 }
 
 template <bool PAIR, int BN, typename Y>
@@ -763,18 +755,8 @@ cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, in
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(W::kCtas * std::min<int64_t>(tiles, sms / W::kCtas)));
-    cfg.blockDim = dim3(kWideThreads);
-    cfg.dynamicSmemBytes = W::smem(a.E);
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = W::kCtas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, tmx, tmw);
+    const unsigned grid = (unsigned)(W::kCtas * std::min<int64_t>(tiles, sms / W::kCtas));
+    return launch_overlapped(kern, grid, kWideThreads, W::smem(a.E), st, (unsigned)W::kCtas, a, tmx, tmw);
 }
 
 template <typename Y>

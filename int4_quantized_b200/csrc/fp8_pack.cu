@@ -47,9 +47,11 @@ Q4_DEVINL void unpack16(const uint4 &r, float *v) {
     }
 }
 
-// 32 bytes (a whole sector) in one load.
+// 32 bytes (a whole sector) in one load. Volatile and not .nc: it stays behind the wait for the
+// kernel before (launch_overlapped), and so do the plain loads, whose pointers are not
+// __restrict__.
 Q4_DEVINL void ld_v8(const void *p, uint4 &a, uint4 &b) {
-    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
         : "l"(p));
 }
@@ -205,6 +207,7 @@ struct RowsArgs {
 
 template <typename T, bool SILU, bool VEC, int U>
 __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
+    begin_overlapped();
     const int sub = threadIdx.x & 7;
     const uint32_t first = blockIdx.x * (32 * U) + (threadIdx.x >> 3);
     const uint32_t live = a.count ? (uint32_t)max(*a.count, 0) : UINT32_MAX;
@@ -301,10 +304,11 @@ __global__ void __launch_bounds__(256) fp8_pack_rows(const RowsArgs a) {
 // of 64 values one CTA filled the registers and nothing covered its loads).
 constexpr int kTileThreads = 512;
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *__restrict__ w, int64_t N, int64_t K, uint32_t nb,
-                                                      uint32_t kb, uint8_t *__restrict__ codes,
-                                                      float *__restrict__ scales, uint32_t *status) {
+__global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *w, int64_t N, int64_t K, uint32_t nb,
+                                                      uint32_t kb, uint8_t *codes,
+                                                      float *scales, uint32_t *status) {
     constexpr int PER = 32 / sizeof(T), LANES = 128 / PER, ROWS = kTileThreads / LANES, STEPS = 128 / ROWS;
+    begin_overlapped();
     const uint32_t t = blockIdx.x / kb, kblk = blockIdx.x - t * kb;  // t: (matrix, row block)
     const uint32_t e = t / nb, nblk = t - e * nb;
     const int64_t k0 = (int64_t)kblk * 128 + (threadIdx.x % LANES) * PER;
@@ -373,16 +377,22 @@ cudaError_t pack_rows(const RowsArgs &a, bool silu, cudaStream_t st) {
     // than fill the machine so, one each (16 x 4096: 16 CTAs instead of 8)
     const bool two = a.units >= 148 * 32 * 2 * 2;
     const unsigned grid = (a.units + (two ? 63 : 31)) / (two ? 64 : 32);
-#define Q4_ROWS(S, V, U) fp8_pack_rows<T, S, V, U><<<grid, 256, 0, st>>>(a)
-    if (silu) {
-        if (vec) two ? Q4_ROWS(true, true, 2) : Q4_ROWS(true, true, 1);
-        else two ? Q4_ROWS(true, false, 2) : Q4_ROWS(true, false, 1);
-    } else {
-        if (vec) two ? Q4_ROWS(false, true, 2) : Q4_ROWS(false, true, 1);
-        else two ? Q4_ROWS(false, false, 2) : Q4_ROWS(false, false, 1);
+#define Q4_ROWS(S, V, U) return launch_overlapped(fp8_pack_rows<T, S, V, U>, grid, 256, 0, st, 1, a)
+    if (two) {
+        if (silu) {
+            if (vec) Q4_ROWS(true, true, 2);
+            Q4_ROWS(true, false, 2);
+        }
+        if (vec) Q4_ROWS(false, true, 2);
+        Q4_ROWS(false, false, 2);
     }
+    if (silu) {
+        if (vec) Q4_ROWS(true, true, 1);
+        Q4_ROWS(true, false, 1);
+    }
+    if (vec) Q4_ROWS(false, true, 1);
+    Q4_ROWS(false, false, 1);
 #undef Q4_ROWS
-    return cudaGetLastError();
 }
 
 template <typename T>
@@ -391,11 +401,9 @@ cudaError_t pack_tiles(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *
     const bool vec = (K * (int64_t)sizeof(T)) % 32 == 0 && (uintptr_t)w % 32 == 0 && (uintptr_t)codes % 16 == 0;
     const uint32_t nb = (uint32_t)((N + 127) / 128), kb = (uint32_t)((K + 127) / 128);
     const unsigned grid = (unsigned)(E * nb * kb);
-    if (vec)
-        fp8_pack_tiles<T, true><<<grid, kTileThreads, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
-    else
-        fp8_pack_tiles<T, false><<<grid, kTileThreads, 0, st>>>(static_cast<const T *>(w), N, K, nb, kb, codes, scales, status);
-    return cudaGetLastError();
+    auto kern = vec ? fp8_pack_tiles<T, true> : fp8_pack_tiles<T, false>;
+    return launch_overlapped(kern, grid, kTileThreads, 0, st, 1, static_cast<const T *>(w), N, K, nb, kb, codes, scales,
+                             status);
 }
 
 // Blocks of a call, at most 2^31 - 1 (such codes alone would be 275 GB).

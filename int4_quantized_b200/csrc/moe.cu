@@ -19,6 +19,8 @@
 //                     slots, dys[pos] = w dout is written and dw = <dout, ys[pos]> summed.
 // All but the sort are bound by the rows they read and write; each lane has up to 8 accesses
 // of 16 bytes on their way.
+// No pointer is __restrict__: inputs may come from a kernel that still runs when these start
+// (launch_overlapped), so no load may be taken for invariant and moved over the wait.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -65,10 +67,11 @@ Q4_DEVINL uint32_t same_lanes(int e, int bits) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kSortWarps) moe_sort_kernel(const T *__restrict__ ids, int64_t R, int k, int E,
-                                                                   int32_t *__restrict__ tokens,
-                                                                   int32_t *__restrict__ pos,
-                                                                   int32_t *__restrict__ offsets) {
+__global__ void __launch_bounds__(32 * kSortWarps) moe_sort_kernel(const T *ids, int64_t R, int k, int E,
+                                                                   int32_t *tokens,
+                                                                   int32_t *pos,
+                                                                   int32_t *offsets) {
+    begin_overlapped();
     extern __shared__ int32_t sm[];
     const int W = blockDim.x >> 5;
     int32_t *hist = sm;            // [W][E]: counts, then each warp's next place after the warps before it
@@ -220,9 +223,10 @@ Q4_DEVINL void store_once(V *p, V v) {
 
 // A warp copies P parts of 32 accesses from each of kInFlight / P rows.
 template <typename V, int P>
-__global__ void __launch_bounds__(256) moe_gather_kernel(const V *__restrict__ x, int64_t T,
-                                                         const int32_t *__restrict__ tokens, int64_t R, int64_t per_row,
-                                                         uint32_t chunks, V *__restrict__ xs) {
+__global__ void __launch_bounds__(256) moe_gather_kernel(const V *x, int64_t T,
+                                                         const int32_t *tokens, int64_t R, int64_t per_row,
+                                                         uint32_t chunks, V *xs) {
+    begin_overlapped();
     constexpr int ROWS = kGatherInFlight / P;
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t g = unit / chunks, ch = unit - g * chunks;
@@ -250,13 +254,14 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const V *__restrict__ x
 
 // A warp sums P parts of 32 accesses of a row, S slots at a time.
 template <typename T, int B, int S, int P>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, B>::V *__restrict__ ys, int64_t R,
-                                                          const int32_t *__restrict__ pos,
-                                                          const float *__restrict__ weights, int64_t tokens, int k,
+__global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, B>::V *ys, int64_t R,
+                                                          const int32_t *pos,
+                                                          const float *weights, int64_t tokens, int k,
                                                           int64_t per_row, uint32_t chunks,
-                                                          typename Row<T, B>::V *__restrict__ out) {
+                                                          typename Row<T, B>::V *out) {
     using V = typename Row<T, B>::V;
     constexpr int N = Row<T, B>::N;
+    begin_overlapped();
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const uint32_t t = unit / chunks, ch = unit - t * chunks;
     if (t >= tokens) return;
@@ -299,14 +304,15 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const typename Row<T, 
 
 // W warps take one token, S slots at a time and P accesses of each; 4 / W tokens a CTA.
 template <typename T, int B, int W, int S, int P>
-__global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, B>::V *__restrict__ dout,
-                                                       const typename Row<T, B>::V *__restrict__ ys, int64_t R,
-                                                       const int32_t *__restrict__ pos,
-                                                       const float *__restrict__ weights, int64_t tokens, int k,
-                                                       int64_t per_row, typename Row<T, B>::V *__restrict__ dys,
-                                                       float *__restrict__ dweights) {
+__global__ void __launch_bounds__(128) moe_combine_bwd(const typename Row<T, B>::V *dout,
+                                                       const typename Row<T, B>::V *ys, int64_t R,
+                                                       const int32_t *pos,
+                                                       const float *weights, int64_t tokens, int k,
+                                                       int64_t per_row, typename Row<T, B>::V *dys,
+                                                       float *dweights) {
     using V = typename Row<T, B>::V;
     constexpr int N = Row<T, B>::N;
+    begin_overlapped();
     __shared__ float part[4][S];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (4 / W) + warp / W, s0 = t * k;
@@ -395,18 +401,8 @@ cudaError_t sort_launch(const void *ids, int64_t R, int k, int E, int32_t *token
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T *>(ids), R, k, E, tokens, pos, offsets);
+    return launch_overlapped(kern, ctas, 32 * warps, smem, st, ctas, static_cast<const T *>(ids), R, k, E, tokens, pos,
+                             offsets);
 }
 
 // Parts of 32 accesses that a warp takes of a row of per_row accesses: at most `most`, a power of 2.
@@ -432,15 +428,14 @@ cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64
     const unsigned grid = row_grid(groups, chunks);
     *fits = grid != 0;
     if (!grid) return cudaSuccess;
-#define Q4_GATHER(P_)                                                                                              \
-    moe_gather_kernel<V, P_><<<grid, 256, 0, st>>>(static_cast<const V *>(x), T, tokens, R, per_row, (uint32_t)chunks, \
-                                                   static_cast<V *>(xs))
+#define Q4_GATHER(P_)                                                                                             \
+    return launch_overlapped(moe_gather_kernel<V, P_>, grid, 256, 0, st, 1, static_cast<const V *>(x), T, tokens, R, \
+                             per_row, (uint32_t)chunks, static_cast<V *>(xs))
     if (P == 1) Q4_GATHER(1);
     else if (P == 2) Q4_GATHER(2);
     else if (P == 4) Q4_GATHER(4);
     else Q4_GATHER(8);
 #undef Q4_GATHER
-    return cudaGetLastError();
 }
 
 template <typename T, int B>
@@ -455,9 +450,9 @@ cudaError_t combine_rows(const void *ys, int64_t R, const int32_t *pos, const fl
     const unsigned grid = row_grid(tokens, chunks);
     *fits = grid != 0;
     if (!grid) return cudaSuccess;
-#define Q4_COMBINE(S_, P_)                                                                                          \
-    moe_combine_kernel<T, B, S_, P_><<<grid, 256, 0, st>>>(static_cast<const V *>(ys), R, pos, weights, tokens, k, \
-                                                           per_row, (uint32_t)chunks, static_cast<V *>(out))
+#define Q4_COMBINE(S_, P_)                                                                                       \
+    return launch_overlapped(moe_combine_kernel<T, B, S_, P_>, grid, 256, 0, st, 1, static_cast<const V *>(ys), R, \
+                             pos, weights, tokens, k, per_row, (uint32_t)chunks, static_cast<V *>(out))
     if (P == 16) Q4_COMBINE(1, 16);
     else if (P == 8 && k == 1) Q4_COMBINE(1, 8);
     else if (P == 8) Q4_COMBINE(2, 8);
@@ -466,7 +461,6 @@ cudaError_t combine_rows(const void *ys, int64_t R, const int32_t *pos, const fl
     else if (P == 2) Q4_COMBINE(4, 2);
     else Q4_COMBINE(8, 1);
 #undef Q4_COMBINE
-    return cudaGetLastError();
 }
 
 template <typename T>
@@ -483,10 +477,10 @@ cudaError_t bwd_rows(const void *dout, const void *ys, int64_t R, const int32_t 
                      int64_t tokens, int k, int64_t D, void *dys, float *dweights, cudaStream_t st) {
     using V = typename Row<T, B>::V;
     const int64_t per_row = D / Row<T, B>::N;
-#define Q4_BWD(W_, S_, P_)                                                                                           \
-    moe_combine_bwd<T, B, W_, S_, P_><<<(unsigned)((tokens + 4 / W_ - 1) / (4 / W_)), 128, 0, st>>>(                 \
-        static_cast<const V *>(dout), static_cast<const V *>(ys), R, pos, weights, tokens, k, per_row,               \
-        static_cast<V *>(dys), dweights)
+#define Q4_BWD(W_, S_, P_)                                                                                            \
+    return launch_overlapped(moe_combine_bwd<T, B, W_, S_, P_>, (unsigned)((tokens + 4 / W_ - 1) / (4 / W_)), 128, 0,  \
+                             st, 1, static_cast<const V *>(dout), static_cast<const V *>(ys), R, pos, weights, tokens, \
+                             k, per_row, static_cast<V *>(dys), dweights)
     // rows below 128 accesses leave three of four warps idle: one warp a token there
     // (65536 tokens x 8 of 256 bf16 values: 290 us with four, 129 with one)
     constexpr int M = B == 16 ? 1 : 4;
@@ -498,7 +492,6 @@ cudaError_t bwd_rows(const void *dout, const void *ys, int64_t R, const int32_t 
         else Q4_BWD(1, 8, 1);
     }
 #undef Q4_BWD
-    return cudaGetLastError();
 }
 
 template <typename T>

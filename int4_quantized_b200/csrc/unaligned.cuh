@@ -31,8 +31,8 @@ Q4_DEVINL uint4 load_any16(const void *p, int n) {
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
     const uint32_t sh = (uint32_t)(uintptr_t)p & 15;
     const uint4 *a = reinterpret_cast<const uint4 *>((uintptr_t)p - sh);
-    if (n > 0) lo = __ldg(a);
-    if ((int)sh + min(n, 16) > 16) hi = __ldg(a + 1);
+    if (n > 0) lo = *a;
+    if ((int)sh + min(n, 16) > 16) hi = a[1];
     const uint4 v = shift_bytes(lo, hi, sh);
     return n < 16 ? first_bytes(v, n) : v;
 }

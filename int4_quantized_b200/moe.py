@@ -150,7 +150,9 @@ class Fp8Experts:
         tokens, pos, offsets = moe_sort(ids, self.E)
         live = offsets[self.E:]  # rows that have an expert
         xq, xs = fp8_pack(x, rows=tokens, status=status)
-        h = fp8_gemm_grouped(xq, xs, self.gate_up, self.gate_up_scales, offsets, out_dtype=x.dtype, status=status)
+        # gate and up become codes of 4 bits next: bf16 keeps enough of them, and unlike fp16 their range
+        between = torch.bfloat16 if x.dtype == torch.float16 else x.dtype
+        h = fp8_gemm_grouped(xq, xs, self.gate_up, self.gate_up_scales, offsets, out_dtype=between, status=status)
         hq, hs = fp8_pack(h, count=live, silu_mul=True, status=status)
         ys = fp8_gemm_grouped(hq, hs, self.down, self.down_scales, offsets, out_dtype=x.dtype, status=status)
         return moe_combine(ys, pos, weights)

@@ -122,7 +122,7 @@ def test_pack_quotients_exactly(q4):
 
 
 @pytest.mark.parametrize("x_type", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,K", [(3, 128), (5, 100), (2, 1), (9, 1032), (40, 14336)])
+@pytest.mark.parametrize("M,K", [(3, 128), (5, 100), (2, 1), (9, 1032), (40, 14336), (3, 333), (301, 4099)])
 def test_pack_silu_mul(q4, x_type, M, K):
     import torch
 

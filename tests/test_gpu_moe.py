@@ -221,7 +221,8 @@ def test_refusals(q4):
 def experts_ref(q4, layer, x, ids, w):
     """The layer in 64 bits from the same codes, and how far each rounding on the way may move it.
 
-    Rounded on the way: x to codes (the oracle's are the same, bit for bit), h to x's type, the
+    Rounded on the way: x to codes (the oracle's are the same, bit for bit), h to x's type (bf16
+    where that is fp16), the
     activation to codes, the answers to x's type, and the sum. Returns (out, the sum over the
     experts of the weighted answers' bounds)."""
     import torch
@@ -231,6 +232,7 @@ def experts_ref(q4, layer, x, ids, w):
     xc, xs = fp8.pack(xn)
     a = fp8.dequant(xc, xs)
     h_step = torch.finfo(x.dtype).eps / 2
+    between = torch.finfo(torch.bfloat16).eps / 2 if x.dtype == torch.float16 else h_step  # of gate and up
     gu, gus, dn, dns = u8(layer.gate_up), layer.gate_up_scales.cpu().numpy(), u8(layer.down), layer.down_scales.cpu().numpy()
     out, bound = np.zeros((len(xn), layer.D)), np.zeros((len(xn), layer.D))
     for t in range(len(xn)):
@@ -240,7 +242,7 @@ def experts_ref(q4, layer, x, ids, w):
                 continue
             b, d = fp8.dequant(gu[e], gus[e], 128), fp8.dequant(dn[e], dns[e], 128)
             h, hm = b @ a[t], np.abs(b) @ np.abs(a[t])
-            dh = h_step * np.abs(h) + 2.0 ** -15 * hm  # rounding of h, and the fp32 sums (2^-23 x (128 + 2 x blocks + 8) < 2^-15)
+            dh = between * np.abs(h) + 2.0 ** -15 * hm  # rounding of h, and the fp32 sums (2^-23 x (128 + 2 x blocks + 8) < 2^-15)
             F = layer.F
             act = fp8.silu_mul(h[None])[0]
             g, u = h[:F], h[F:]
@@ -292,6 +294,20 @@ def test_experts(q4, T, k, E, D, F, x_type):
     torch.cuda.synchronize()
     y64f = y64[::-1]
     assert np.linalg.norm(again.double().cpu().numpy() - y64f) <= 2.0 ** -4 * np.linalg.norm(y64f)
+
+
+def test_experts_wide_values_in_fp16(q4):
+    # gate and up beyond fp16's range between the products, answers inside it
+    import torch
+
+    layer = q4.Fp8Experts.pack(torch.full((1, 64, 64), 40.0, device="cuda"), torch.full((1, 64, 32), 2.0 ** -24, device="cuda"))
+    x = torch.full((2, 64), 50.0, device="cuda", dtype=torch.float16)  # gate = up = 128000
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = layer(x, torch.zeros(2, 1, dtype=torch.int64, device="cuda"), torch.ones(2, 1, device="cuda"), status=status)
+    want = 128000.0 ** 2 * 32 * 2.0 ** -24
+    assert int(status.item()) == 0
+    # three bf16 or fp16 roundings (gate, up, the answer); the codes are the blocks' largest values, 448
+    assert bool(((out.double() - want).abs() <= want * (2 * 2.0 ** -8 + 2.0 ** -11) * 1.01).all())
 
 
 def test_experts_refusals(q4):
