@@ -57,7 +57,8 @@ struct Fp8Args {
     int32_t R, E;
     int32_t nb, kb;          // blocks of 128 along N and K
     int32_t split;           // CTAs of a cluster that share one tile's K
-    int32_t stages;          // ring depth
+    int32_t stages;          // ring depth (fp8_stream)
+    int32_t box;             // rows of x a copy brings (fp8_wide): 128, fewer where x has fewer
 };
 
 // The experts' rows and tiles, worked out once a block: expert e has the rows rows0[e] ..
@@ -537,6 +538,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             if (lane == 0) {
                 Slot s;
                 int filled = 0;
+                const uint32_t bytes = (uint32_t)(W::kCtas * (W::kStage - (128 - a.box) * kBK));
                 for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
                     const Tile t = tile_at(a, W::kRows, cols, first, rows0, j);
                     const int wrow = (int)(t.e * a.N + (int64_t)t.nb * BN + rank * W::kOwnCols);
@@ -546,7 +548,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                         if (timed_out) break;
                         uint8_t *st = ring + s.i * W::kStage;
                         // of a pair, the first CTA's barrier counts the bytes of both
-                        if (rank == 0) mbar_arrive_expect_tx(full + s.i, W::kCtas * W::kStage);
+                        if (rank == 0) mbar_arrive_expect_tx(full + s.i, bytes);
                         if constexpr (PAIR) {
                             const uint32_t bar = map_rank(smem_u32(full + s.i), 0);
                             tma_load_2d_pair(st, &tmx, bar, kb * kBK, xrow);
@@ -737,11 +739,14 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
 }
 
 template <bool PAIR, int BN, typename Y>
-cudaError_t launch_wide(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
+cudaError_t launch_wide(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     using W = Wide<PAIR, BN>;
     const int64_t tiles = row_tiles(a, W::kRows) * ((a.N + BN - 1) / BN);
+    // What a smaller box leaves of the x tile in shared memory is any codes: rows of D that are
+    // not stored
+    a.box = (int)std::min<int64_t>(128, (a.R + 7) / 8 * 8);
     CUtensorMap tmx, tmw;
-    if (!encode_codes_map(&tmx, x, a.R, K, 128) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, W::kOwnCols))
+    if (!encode_codes_map(&tmx, x, a.R, K, a.box) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, W::kOwnCols))
         return cudaErrorInvalidValue;
     auto kern = fp8_wide<PAIR, BN, Y>;
     static std::atomic<uint64_t> ready{0};
@@ -816,7 +821,7 @@ q4_status fp8_product(const uint8_t *x, const float *xs, int64_t R, const int32_
     if (!x || !xs || !w || !ws || !y) return Q4_ERR_ARG;
     if ((uintptr_t)x % 16 || (uintptr_t)w % 16) return Q4_ERR_UNSUPPORTED;
     Fp8Args a{xs, ws, offsets, y, status, N, (int32_t)R, (int32_t)E, (int32_t)((N + 127) / 128),
-              (int32_t)((K + 127) / 128), 1, 0};
+              (int32_t)((K + 127) / 128), 1, 0, 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int sms = device_sms();
     const cudaError_t e = yt == Q4_F32    ? launch_fp8<float>(a, x, w, K, sms, st)
