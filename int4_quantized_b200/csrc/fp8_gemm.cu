@@ -767,9 +767,9 @@ cudaError_t launch_wide(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K
 template <typename Y>
 cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     if (a.offsets) {
-        // Up to 32 rows: fp8_stream (64 experts of 1408 x 2048, 8 rows: 10.5 us, fp8_wide 11.8;
-        // 32 rows: 16.6, 18.4; but 64 rows: 33.4, 28.8)
-        if (a.R <= 32) return launch_stream<16, Y>(a, x, w, K, sms, st);
+        // Up to 8 rows: fp8_stream, which splits K (64 experts of 1408 x 2048, 1 row: 7.8 us,
+        // fp8_wide 11.3; 8 rows: 9.9 and 11.9; but 32 rows: 15.9 and 13.9, 64 rows: 31.6 and 26.8)
+        if (a.R <= 8) return launch_stream<16, Y>(a, x, w, K, sms, st);
     } else {
         // Few rows: fp8_stream where its tiles leave SMs to split K over (11008 x 4096, 16 rows:
         // 16.0 us, fp8_wide 18.5; 4096 x 11008, 128 rows: 26.0 and 33.9; but 4096 x 4096, 200
