@@ -433,6 +433,10 @@ constexpr int kWideThreads = 384;  // TMA, MMA, two without a role, eight epilog
 constexpr int kWideRegs = 168, kWideLow = 72, kWideHigh = 216;
 static_assert(128 * kWideLow + 256 * kWideHigh == kWideThreads * kWideRegs, "register split");
 
+// Shared memory in which an epilogue warp turns 32 rows x 64 bytes of y, 4 bytes a row apart
+// from the banks of the last.
+constexpr int kTurnRow = 68, kTurnBytes = 32 * kTurnRow;
+
 // A tile of BN weight rows, made by one CTA or a pair.
 template <bool PAIR, int BN>
 struct Wide {
@@ -445,9 +449,11 @@ struct Wide {
     static constexpr int kBufs = 512 / BN;    // all 512 columns of tensor memory
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
     static size_t smem(int E) {
-        return 1024 + (size_t)kStages * kStage + (2 * kStages + 2 * kBufs + 1) * 8 + 16 + (size_t)(2 * E + 2) * 4;
+        return 1024 + (size_t)kStages * kStage + 8 * kTurnBytes + (2 * kStages + 2 * kBufs + 1) * 8 + 16 +
+               (size_t)(2 * E + 2) * 4;
     }
 };
+
 
 template <bool PAIR>
 Q4_DEVINL void umma_f8_of(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
@@ -484,7 +490,8 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
     constexpr int HALF = BN / 2;  // columns an epilogue warp keeps
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + W::kStages * W::kStage);
+    uint8_t *turn = ring + W::kStages * W::kStage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(turn + 8 * kTurnBytes);
     uint64_t *empty = full + W::kStages;
     uint64_t *dfull = empty + W::kStages;
     uint64_t *dempty = dfull + W::kBufs;
@@ -644,26 +651,46 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                 }
                 d.next(W::kBufs);
             }
-            if (!live || timed_out) continue;
+            if (timed_out) continue;
             auto value = [&](int c) {
                 return __uint_as_float((c & 1) ? (uint32_t)(acc[c >> 1] >> 32) : (uint32_t)acc[c >> 1]);
             };
-            Y *yr = y + (int64_t)(t.row0 + rl) * a.N + n0;
+            auto word = [&](int c) {  // the 4 bytes of y from column c on
+                if constexpr (sizeof(Y) == 4) return __float_as_uint(value(c));
+                else return two<Y>(value(c), value(c + 1));
+            };
+            constexpr int IN4 = 4 / (int)sizeof(Y);  // columns in 4 bytes
             if (vec) {
+                Y *yr = y + (int64_t)(t.row0 + rl) * a.N + n0;
 #pragma unroll
                 for (int c = 0; c < HALF; c += PER) {
                     uint32_t v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if constexpr (sizeof(Y) == 4) v[i] = __float_as_uint(value(c + i));
-                        else v[i] = two<Y>(value(c + 2 * i), value(c + 2 * i + 1));
-                    }
-                    if (n0 + c < a.N) st_v8(yr + c, v);
+                    for (int i = 0; i < 8; ++i) v[i] = word(c + i * IN4);
+                    if (live && n0 + c < a.N) st_v8(yr + c, v);
                 }
             } else {
+                // Rows of y that are not whole 32-byte stores: single elements, but a warp's 32 (or,
+                // of fp32, 16 of two rows) side by side, not in 32 rows (4099 x 7801 x 880 in fp16:
+                // 348 us so)
+                constexpr int CH = 64 / (int)sizeof(Y);
+                uint8_t *mine = turn + (warp - 4) * kTurnBytes;
+                const int col = lane % CH, up = lane / CH, first_row = rl - lane;
 #pragma unroll
-                for (int c = 0; c < HALF; ++c)
-                    if (n0 + c < a.N) yr[c] = round_to<Y>(value(c));
+                for (int c = 0; c < HALF; c += CH) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        *reinterpret_cast<uint32_t *>(mine + lane * kTurnRow + 4 * i) = word(c + i * IN4);
+                    __syncwarp();
+                    const int rows = min(32, t.rows - first_row);
+                    if (n0 + c + col < a.N) {
+                        Y *yc = y + (int64_t)(t.row0 + first_row) * a.N + n0 + c + col;
+#pragma unroll 8
+                        for (int r = up; r < rows; r += 32 / CH)
+                            yc[(int64_t)r * a.N] = *reinterpret_cast<const Y *>(mine + r * kTurnRow + col * sizeof(Y));
+                    }
+                    __syncwarp();
+                }
             }
         }
     }
