@@ -672,7 +672,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             } else {
                 // Rows of y that are not whole 32-byte stores: single elements, but a warp's 32 (or,
                 // of fp32, 16 of two rows) side by side, not in 32 rows (4099 x 7801 x 880 in fp16:
-                // 348 us so)
+                // 348 us so, 58 this way)
                 constexpr int CH = 64 / (int)sizeof(Y);
                 uint8_t *mine = turn + (warp - 4) * kTurnBytes;
                 const int col = lane % CH, up = lane / CH, first_row = rl - lane;
@@ -794,9 +794,10 @@ cudaError_t launch_wide(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K
 template <typename Y>
 cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     if (a.offsets) {
-        // Up to 8 rows: fp8_stream, which splits K (64 experts of 1408 x 2048, 1 row: 7.8 us,
-        // fp8_wide 11.3; 8 rows: 9.9 and 11.9; but 32 rows: 15.9 and 13.9, 64 rows: 31.6 and 26.8)
-        if (a.R <= 8) return launch_stream<16, Y>(a, x, w, K, sms, st);
+        // A few rows: fp8_stream, which splits K (weights from HBM, 4 rows: 8 experts of 4096 x 14336
+        // 38.2 us, fp8_wide 50.5; 64 of 1408 x 2048: 9.1 and 11.8; but 8 rows: 76.3 and 55.7, 10.5
+        // and 12.4; 16 rows: 79.4 and 75.9, 16.9 and 13.9; 64 rows: 80.1 and 76.4, 27.7 and 26.0)
+        if (a.R < 8) return launch_stream<16, Y>(a, x, w, K, sms, st);
     } else {
         // Few rows: fp8_stream where its tiles leave SMs to split K over (11008 x 4096, 16 rows:
         // 16.0 us, fp8_wide 18.5; 4096 x 11008, 128 rows: 26.0 and 33.9; but 4096 x 4096, 200
