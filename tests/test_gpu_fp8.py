@@ -477,3 +477,53 @@ def test_two_products_at_once(q4):
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert torch.equal(w, o)
+
+
+def test_offsets_beyond_32_bits(q4):
+    # codes, and y, of more than 2^32 elements: the far rows are those of the near ones
+    import torch
+
+    x = torch.randn(7, 4096, device="cuda")
+    R = 1 << 20 | 5
+    rows = (torch.arange(R, device="cuda") % 7).int()
+    codes, scales = q4.fp8_pack(x, rows=rows)
+    near, near_s = q4.fp8_pack(x)
+    assert codes.numel() > 1 << 32
+    for i in (0, R // 2, R - 1):
+        assert torch.equal(codes[i].view(torch.uint8), near[i % 7].view(torch.uint8)) and torch.equal(scales[i], near_s[i % 7])
+    del codes, scales
+    M, N, K = 70001, 65552, 16
+    _, (xc, xs, w, ws) = problem(5, 64, 80, K)
+    x = xc.view(torch.uint8).repeat(-(-M // 64), 1)[:M].contiguous().view(torch.float8_e4m3fn)
+    w = w.view(torch.uint8).repeat(-(-N // 80), 1)[:N].contiguous().view(torch.float8_e4m3fn)
+    xs = xs.repeat(-(-M // 64), 1)[:M].contiguous()
+    ws = torch.ones(q4.fp8._blocks(N), 1, device="cuda")
+    y = q4.fp8_gemm(x, xs, w, ws)
+    assert y.numel() > 1 << 32
+    near = q4.fp8_gemm(x[:64].contiguous(), xs[:64].contiguous(), w[:80].contiguous(), ws[:1].contiguous())
+    for m in (0, 40000, M - 1):
+        assert torch.equal(y[m, :80], near[m % 64]) and torch.equal(y[m, N - 32:], near[m % 64, (N - 32) % 80:][:32])
+
+
+def test_static_weights_after_these_kernels(q4):
+    # qpack, one of these kernels, then qgemm with its weights declared static: the promise (packed
+    # before the kernel in between began) holds, because that kernel lets the next one come on only
+    # when all before it is done
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.randn(8192, 8192, device="cuda", generator=g)
+    small, x = torch.randn(4, 256, device="cuda", generator=g), torch.randn(1, 8192, device="cuda", generator=g)
+    payload, scales = q4.qpack(w, 4, 128)
+    want = q4.qgemm(x, payload, scales, 8192, 8192, 4, 128)
+    c, s = q4.fp8_pack_weights(small)
+    ids = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    between = [lambda: q4.fp8_pack(small), lambda: q4.fp8_pack_weights(small), lambda: q4.moe_sort(ids, 2),
+               lambda: q4.moe_gather(small, ids[0]), lambda: q4.moe_combine(small, ids), lambda: q4.fp8_gemm(*q4.fp8_pack(small), c, s)]
+    for f in between:
+        for _ in range(3):
+            payload.zero_()
+            q4.qpack(w, 4, 128, payload=payload, scales=scales)
+            f()
+            y = q4.qgemm(x, payload, scales, 8192, 8192, 4, 128, weights_static=True)
+            assert torch.equal(y, want)

@@ -323,3 +323,53 @@ def test_experts_refusals(q4):
                 lambda: q4.Fp8Experts(layer.gate_up, layer.gate_up_scales[:1], layer.down, layer.down_scales)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_offsets_beyond_32_bits(q4):
+    import torch
+
+    T, D, R = 5, 4096, 1 << 20 | 3
+    x = torch.randn(T, D, device="cuda").bfloat16()
+    tokens = (torch.arange(R, device="cuda") % T).int()
+    xs = q4.moe_gather(x, tokens)
+    assert xs.numel() > 1 << 32
+    for i in (0, R // 2, R - 1):
+        assert torch.equal(xs[i], x[i % T])
+    pos = torch.tensor([[0, R - 1], [R - 1, R - 2]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5, 0.25], [1.0, 2.0]], device="cuda")
+    out = q4.moe_combine(xs, pos, w)
+    want = (xs[pos.long()].double() * w[..., None].double()).sum(1)
+    assert bool(((out.double() - want).abs() <= want.abs() * 2.0 ** -8 + 2.0 ** -20 * 8).all())
+    del out
+    dout = torch.randn(2, D, device="cuda").bfloat16()
+    pos = torch.tensor([[0, R - 1], [R // 2, R - 2]], dtype=torch.int32, device="cuda")
+    dys, dw = q4.moe_combine_backward(dout, xs, pos, w)
+    for t in range(2):
+        for j in range(2):
+            p = int(pos[t, j])
+            assert torch.equal(dys[p], (dout[t].float() * w[t, j]).bfloat16())
+            ref = (dout[t].double() * xs[p].double()).sum()
+            assert abs(float(dw[t, j]) - float(ref)) <= D * 2.0 ** -24 * float((dout[t].double() * xs[p].double()).abs().sum())
+
+
+def test_experts_on_two_streams_and_graphs(q4):
+    # nothing is shared between calls: two captured layers replayed together give what one gives
+    import torch
+
+    layer = q4.Fp8Experts.pack(torch.randn(4, 128, 64, device="cuda") / 8, torch.randn(4, 64, 64, device="cuda") / 8)
+    args = [(torch.randn(n, 64, device="cuda"), torch.randint(-1, 4, (n, 2), device="cuda"), torch.rand(n, 2, device="cuda")) for n in (3, 300)]
+    want = [layer(*a) for a in args]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer(*a))
+        graphs.append(g)
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
