@@ -30,7 +30,8 @@ def _dtype(t: torch.dtype, name: str) -> int:
 
 def _arg(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """Device pointer of a contiguous CUDA tensor of this dtype and shape (None: any) on this device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.device != device or (
+    # get_device() is -1 off the GPU, and half as dear as comparing devices
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.get_device() != device.index or (
             shape is not None and t.shape != shape):
         _cuda(t, name, dtype)
         if t.device != device:
@@ -50,6 +51,14 @@ def _new(shape, dtype, device) -> torch.Tensor:
             n *= d or 1
         stride.reverse()
     return torch.empty_strided(shape, stride, dtype=dtype, device=device)
+
+
+def _out(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Tuple[torch.Tensor, int]:
+    """An output and its device pointer: the caller's, checked, or a new one."""
+    if t is None:
+        t = _new(shape, dtype, device)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, device)
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -110,13 +119,10 @@ def fp8_pack(x: torch.Tensor, rows: Optional[torch.Tensor] = None, count: Option
         cp = _arg(count, "count", torch.int32, None, dev)
         if count.numel() < 1:
             raise ValueError("count must hold one int32")
-    if codes is None:
-        codes = _new((*lead, K), E4M3, dev)
-    if scales is None:
-        scales = _new((*lead, _blocks(K)), torch.float32, dev)
+    codes, qp = _out(codes, "codes", E4M3, (*lead, K), dev)
+    scales, sp = _out(scales, "scales", torch.float32, (*lead, _blocks(K)), dev)
     _call(dev, "fp8_pack", lib().q4_fp8_pack, x.data_ptr(), xt, n, K, rp, R, cp, FP8_PACK_SILU_MUL if silu_mul else 0,
-          _arg(codes, "codes", E4M3, (*lead, K), dev), _arg(scales, "scales", torch.float32, (*lead, _blocks(K)), dev),
-          _status(status, dev))
+          qp, sp, _status(status, dev))
     return codes, scales
 
 
@@ -133,13 +139,9 @@ def fp8_pack_weights(w: torch.Tensor, codes: Optional[torch.Tensor] = None, scal
     for d in w.shape[:-2]:
         E *= d
     sshape = (*w.shape[:-2], _blocks(N), _blocks(K))
-    if codes is None:
-        codes = _new(w.shape, E4M3, dev)
-    if scales is None:
-        scales = _new(sshape, torch.float32, dev)
-    _call(dev, "fp8_pack_weights", lib().q4_fp8_pack_weights, w.data_ptr(), wt, E, N, K,
-          _arg(codes, "codes", E4M3, w.shape, dev), _arg(scales, "scales", torch.float32, sshape, dev),
-          _status(status, dev))
+    codes, qp = _out(codes, "codes", E4M3, w.shape, dev)
+    scales, sp = _out(scales, "scales", torch.float32, sshape, dev)
+    _call(dev, "fp8_pack_weights", lib().q4_fp8_pack_weights, w.data_ptr(), wt, E, N, K, qp, sp, _status(status, dev))
     return codes, scales
 
 
@@ -153,14 +155,13 @@ def fp8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales:
     dev = x.device
     N, K = w.shape
     lead = tuple(x.shape[:-1])
-    if out is None:
-        out = _new((*lead, N), out_dtype, dev)
+    out, yp = _out(out, "out", out_dtype if out is None else out.dtype, (*lead, N), dev)
     yt = _dtype(out.dtype, "out")
     kb = _blocks(K)
     _call(dev, "fp8_gemm", lib().q4_fp8_gemm, x.data_ptr(),
           _arg(x_scales, "x_scales", torch.float32, (*lead, kb), dev), x.numel() // K, _arg(w, "w", E4M3, None, dev),
           _arg(w_scales, "w_scales", torch.float32, (_blocks(N), kb), dev), N, K,
-          _arg(out, "out", out.dtype, (*lead, N), dev), yt, _status(status, dev))
+          yp, yt, _status(status, dev))
     return out
 
 
@@ -178,13 +179,12 @@ def fp8_gemm_grouped(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w
     dev = x.device
     R = x.shape[0]
     E, N, K = w.shape
-    if out is None:
-        out = _new((R, N), out_dtype, dev)
+    out, yp = _out(out, "out", out_dtype if out is None else out.dtype, (R, N), dev)
     yt = _dtype(out.dtype, "out")
     kb = _blocks(K)
     _call(dev, "fp8_gemm_grouped", lib().q4_fp8_gemm_grouped, x.data_ptr(),
           _arg(x_scales, "x_scales", torch.float32, (R, kb), dev), R,
           _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E, _arg(w, "w", E4M3, None, dev),
           _arg(w_scales, "w_scales", torch.float32, (E, _blocks(N), kb), dev), N, K,
-          _arg(out, "out", out.dtype, (R, N), dev), yt, _status(status, dev))
+          yp, yt, _status(status, dev))
     return out

@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _cuda, lib
-from .fp8 import E4M3, _arg, _blocks, _call, _dtype, _new, fp8_gemm_grouped, fp8_pack, fp8_pack_weights
+from .fp8 import E4M3, _arg, _blocks, _call, _dtype, _new, _out, fp8_gemm_grouped, fp8_pack, fp8_pack_weights
 
 
 def moe_sort(ids: torch.Tensor, num_experts: int) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
@@ -54,10 +54,9 @@ def moe_gather(x: torch.Tensor, tokens: torch.Tensor, out: Optional[torch.Tensor
     dev = x.device
     T, D = x.shape
     R = tokens.shape[0]
-    if out is None:
-        out = _new((R, D), x.dtype, dev)
+    out, op = _out(out, "out", x.dtype, (R, D), dev)
     _call(dev, "moe_gather", lib().q4_moe_gather, x.data_ptr(), xt, T, D, _arg(tokens, "tokens", torch.int32, None, dev),
-          R, _arg(out, "out", x.dtype, (R, D), dev))
+          R, op)
     return out
 
 
@@ -71,11 +70,10 @@ def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Ten
     dev = ys.device
     R, D = ys.shape
     T, k = pos.shape
-    if out is None:
-        out = _new((T, D), ys.dtype, dev)
+    out, op = _out(out, "out", ys.dtype, (T, D), dev)
     _call(dev, "moe_combine", lib().q4_moe_combine, ys.data_ptr(), yt, R, D, _arg(pos, "pos", torch.int32, None, dev),
           None if weights is None else _arg(weights, "weights", torch.float32, (T, k), dev), T, k,
-          _arg(out, "out", ys.dtype, (T, D), dev))
+          op)
     return out
 
 
@@ -95,13 +93,11 @@ def moe_combine_backward(dout: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor
     dev = ys.device
     R, D = ys.shape
     T, k = pos.shape
-    if dys is None:
-        dys = _new((R, D), ys.dtype, dev)
+    dys, dp = _out(dys, "dys", ys.dtype, (R, D), dev)
     dweights = _new((T, k), torch.float32, dev)
     _call(dev, "moe_combine_backward", lib().q4_moe_combine_backward, _arg(dout, "dout", ys.dtype, (T, D), dev),
           ys.data_ptr(), yt, R, D, _arg(pos, "pos", torch.int32, None, dev),
-          _arg(weights, "weights", torch.float32, (T, k), dev), T, k, _arg(dys, "dys", ys.dtype, (R, D), dev),
-          dweights.data_ptr())
+          _arg(weights, "weights", torch.float32, (T, k), dev), T, k, dp, dweights.data_ptr())
     return dys, dweights
 
 
