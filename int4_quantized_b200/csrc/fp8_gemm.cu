@@ -751,7 +751,11 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     a.stages = (int)((kSmemMax - S::smem(0, a.split, a.E)) / (S::kStage + 16));
     const int64_t blocks = (int64_t)((a.kb + a.split - 1) / a.split) * ((tiles + sms - 1) / sms);
     a.stages = (int)std::max<int64_t>(2, std::min<int64_t>(std::min(a.stages, 16), blocks));
-    const size_t smem = S::smem(a.stages, a.split, a.E);
+    size_t smem = S::smem(a.stages, a.split, a.E);
+    // CTAs of a cluster wait for one another with their tensor memory held: two kernels that could
+    // not both have theirs on an SM must not meet there, or each could hold what the other's
+    // cluster waits for. Over half of the shared memory keeps them apart.
+    if (S::kCols > 128) smem = std::max(smem, kSmemMax / 2 + 1024);
     CUtensorMap tmx, tmw;
     if (!encode_codes_map(&tmx, x, a.R, K, NT) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, kWRows))
         return cudaErrorInvalidValue;

@@ -373,3 +373,42 @@ def test_experts_on_two_streams_and_graphs(q4):
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+def test_captured_fork_and_join(q4):
+    # kernels launched to overlap the one before, captured where what is before them is a copy, a
+    # join of two streams, or nothing
+    import torch
+
+    layer = q4.Fp8Experts.pack(torch.randn(4, 128, 64, device="cuda") / 8, torch.randn(4, 64, 64, device="cuda") / 8)
+    x, ids, w = torch.randn(30, 64, device="cuda"), torch.randint(0, 4, (30, 2), device="cuda"), torch.rand(30, 2, device="cuda")
+    xb = torch.empty_like(x)
+    want = layer(x, ids, w), layer(x * 2, ids, w)
+    pos = torch.arange(60, dtype=torch.int32, device="cuda").view(30, 2)
+    both = q4.moe_combine(torch.stack([want[0], want[1]], 1).view(60, 64), pos)
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = layer(x * 2, ids, w)
+        xb.copy_(x)
+        a = layer(xb, ids, w)
+        c = torch.empty(30, 2, 64, device="cuda")
+        c[:, 0] = a
+        main.wait_stream(side)
+        c[:, 1] = b
+        out = q4.moe_combine(c.view(60, 64), pos)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q = q4.fp8_pack(out)
+        p = q4.fp8_pack(out)
+        main.wait_stream(side)
+        t = q4.moe_sort(ids, 4)  # after a join, with nothing in between
+    for _ in range(5):
+        xb.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(out, both)
+    assert torch.equal(p[0].view(torch.uint8), q[0].view(torch.uint8)) and torch.equal(t[1], q4.moe_sort(ids, 4)[1])
