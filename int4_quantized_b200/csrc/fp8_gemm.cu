@@ -20,8 +20,14 @@
 // pair of CTAs (cta_group::2) one of 256 x 256. In a pair each CTA loads its own rows of x and
 // half of the weights, so that a block of k costs an SM 32 KB from L2 instead of 48 (which
 // single CTAs take at 60 bytes a clock, about all that an SM can); the smaller tiles leave
-// fewer rows empty and fill the machine sooner. Here D's lanes are rows of x, so that the scale of a thread's
-// whole row of D is one number a block of k.
+// fewer rows empty and fill the machine sooner. Here D's lanes are rows of x, so that the
+// scale of a thread's whole row of D is one number a block of k. A block's time is the
+// epilogue's: with two buffers of all columns, an MMA, its epilogue and the signals between
+// them share the time of two blocks (8192 x 4096 x 14336, as first built: no epilogue work 378
+// us, reads of tensor memory only 423, all 466; without waiting for it 318). Tried and slower:
+// two half buffers a block (499 us for 477), 16 epilogue warps (570 for 466), the next columns
+// read while the last are added (registers spill: 514 for 445), spinning waits (474 for 460);
+// y stored by the TMA from shared memory gained 1 to 3 %.
 //   warp 0      TMA producer (of a pair both; all bytes are counted on the first CTA's barriers)
 //   warp 1      tensor memory; MMA issue (in the first CTA, for both)
 //   warps 4-11  promotion and stores: 32 rows x half of the columns a warp, kept in registers; the
@@ -441,19 +447,18 @@ constexpr int kTurnRow = 68, kTurnBytes = 32 * kTurnRow;
 template <bool PAIR, int BN>
 struct Wide {
     static constexpr int kCtas = PAIR ? 2 : 1;
-    static constexpr int kRows = 128 * kCtas;        // rows of x a tile
+    static constexpr int kRows = 128 * kCtas;    // rows of x a tile
     static constexpr int kOwnCols = BN / kCtas;  // weight rows that a CTA loads
     static constexpr int kXBytes = 128 * kBK;
     static constexpr int kStage = kXBytes + kOwnCols * kBK;
     static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 4 of 48
-    static constexpr int kBufs = 512 / BN;    // all 512 columns of tensor memory
+    static constexpr int kBufs = 512 / BN;       // all 512 columns of tensor memory
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
     static size_t smem(int E) {
         return 1024 + (size_t)kStages * kStage + 8 * kTurnBytes + (2 * kStages + 2 * kBufs + 1) * 8 + 16 +
                (size_t)(2 * E + 2) * 4;
     }
 };
-
 
 template <bool PAIR>
 Q4_DEVINL void umma_f8_of(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
