@@ -12,7 +12,7 @@
 //                     hand out the places in slot order (a lane's rank among equal ids of its
 //                     32 slots comes from one vote a bit). One launch, no workspace, and only
 //                     counts are added atomically: the result is the stable order on every run.
-//   moe_gather_kernel one warp copies up to 4 KB: part of a row, or several short rows.
+//   moe_gather_kernel one warp copies up to 2 KB of each of two rows, or several short rows.
 //   moe_combine_kernel out[t] = sum over j of w[t, j] ys[pos[t, j]], in fp32, j ascending,
 //                     rounded once; without weights it is the gradient of the gather.
 //   moe_combine_bwd   four warps or one for each token: dout[t] is read once for all its
@@ -213,8 +213,8 @@ constexpr int kInFlight = B == 16 ? 8 : 16;
 constexpr int kGatherInFlight = 8;  // (16 of an element: 8192 x 4 of 4097 bf16 values 182 us, 8: 114)
 
 // Rows written once: they go first when L2 is full, so that x, which each expert reads again,
-// stays (8192 tokens x 8 of 4096 bf16 values: 132 us without, 122 with; the writes alone take
-// 74). Narrower accesses leave a sector to the next store, so theirs stay too.
+// stays (8192 tokens x 8 of 4096 bf16 values: 132 us without, 122 with, before the chunks'
+// order; the writes alone take 74). Narrower accesses leave a sector to the next store, so theirs stay too.
 template <typename V>
 Q4_DEVINL void store_once(V *p, V v) {
     if constexpr (sizeof(V) == 16) __stcs(p, v);
@@ -225,11 +225,15 @@ Q4_DEVINL void store_once(V *p, V v) {
 template <typename V, int P>
 __global__ void __launch_bounds__(256) moe_gather_kernel(const V *x, int64_t T,
                                                          const int32_t *tokens, int64_t R, int64_t per_row,
-                                                         uint32_t chunks, V *xs) {
+                                                         V *xs) {
     begin_overlapped();
     constexpr int ROWS = kGatherInFlight / P;
     const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const uint32_t g = unit / chunks, ch = unit - g * chunks;
+    // all rows' first chunk, then all rows' second: what the experts read again of x in that time is
+    // one chunk of its rows, which L2 holds (8192 tokens x 8 of 4096 bf16 values, 67 MB of x: row
+    // after row 121 us, chunks of 4 KB 107, of 2 KB 96)
+    const uint32_t groups = (uint32_t)((R + ROWS - 1) / ROWS);
+    const uint32_t ch = unit / groups, g = unit - ch * groups;
     const int64_t v0 = (int64_t)ch * (32 * P) + (threadIdx.x & 31);
     int64_t t[ROWS];
     V r[ROWS][P];
@@ -423,18 +427,17 @@ cudaError_t gather_launch(const void *x, int64_t T, const int32_t *tokens, int64
                           cudaStream_t st, bool *fits) {
     constexpr int F = kGatherInFlight;
     const int64_t per_row = bytes / (int64_t)sizeof(V);
-    const int P = row_parts(per_row, F);
+    const int P = row_parts(per_row, F / 2);
     const int64_t chunks = (per_row + 32 * P - 1) / (32 * P), groups = (R + F / P - 1) / (F / P);
     const unsigned grid = row_grid(groups, chunks);
     *fits = grid != 0;
     if (!grid) return cudaSuccess;
 #define Q4_GATHER(P_)                                                                                             \
     return launch_overlapped(moe_gather_kernel<V, P_>, grid, 256, 0, st, 1, static_cast<const V *>(x), T, tokens, R, \
-                             per_row, (uint32_t)chunks, static_cast<V *>(xs))
+                             per_row, static_cast<V *>(xs))
     if (P == 1) Q4_GATHER(1);
     else if (P == 2) Q4_GATHER(2);
-    else if (P == 4) Q4_GATHER(4);
-    else Q4_GATHER(8);
+    else Q4_GATHER(4);
 #undef Q4_GATHER
 }
 
