@@ -412,3 +412,18 @@ def test_captured_fork_and_join(q4):
     torch.cuda.synchronize()
     assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(out, both)
     assert torch.equal(p[0].view(torch.uint8), q[0].view(torch.uint8)) and torch.equal(t[1], q4.moe_sort(ids, 4)[1])
+
+
+def test_sorted_rows_both_ways(q4):
+    # many rows are packed once and gathered, few are packed in sorted order: the same codes
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for T, k, D in ((4200, 8, 1024), (60, 8, 1024)):
+        x = torch.randn(T, D, device="cuda", generator=g).bfloat16()
+        ids = torch.randint(-1, 16, (T, k), device="cuda", generator=g)
+        tokens, _, offsets = q4.moe_sort(ids, 16)
+        n = int(offsets[-1])
+        got, want = q4.Fp8Experts.sorted_rows(x, tokens), q4.fp8_pack(x, rows=tokens)
+        assert torch.equal(got[0][:n].view(torch.uint8), want[0][:n].view(torch.uint8))
+        assert torch.equal(got[1][:n], want[1][:n])
