@@ -42,6 +42,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "overlap.cuh"
 #include "tcgen05.cuh"
 
 namespace q4 {

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "overlap.cuh"
 #include "unaligned.cuh"
 
 namespace q4 {

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "overlap.cuh"
 
 namespace q4 {
 
