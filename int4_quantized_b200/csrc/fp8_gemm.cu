@@ -26,8 +26,7 @@
 // them share the time of two blocks (8192 x 4096 x 14336, as first built: no epilogue work 378
 // us, reads of tensor memory only 423, all 466; without waiting for it 318). Tried and slower:
 // two half buffers a block (499 us for 477), 16 epilogue warps (570 for 466), the next columns
-// read while the last are added (registers spill: 514 for 445), spinning waits (474 for 460);
-// y stored by the TMA from shared memory gained 1 to 3 %.
+// read while the last are added (registers spill: 514 for 445), spinning waits (474 for 460).
 //   warp 0      TMA producer (of a pair both; all bytes are counted on the first CTA's barriers)
 //   warp 1      tensor memory; MMA issue (in the first CTA, for both)
 //   warps 4-11  promotion and stores: 32 rows x half of the columns a warp, kept in registers; the
@@ -65,6 +64,7 @@ struct Fp8Args {
     int32_t nb, kb;          // blocks of 128 along N and K
     int32_t split;           // CTAs of a cluster that share one tile's K
     int32_t stages;          // ring depth (fp8_stream)
+    int32_t bulk;            // whether the TMA can store y (fp8_wide): rows of whole 16-byte units
     int32_t box;             // rows of x a copy brings (fp8_wide): 128, fewer where x has fewer
 };
 
@@ -444,19 +444,28 @@ static_assert(128 * kWideLow + 256 * kWideHigh == kWideThreads * kWideRegs, "reg
 // from the banks of the last.
 constexpr int kTurnRow = 68, kTurnBytes = 32 * kTurnRow;
 
+// Whether full rows of y leave through shared memory and the TMA, so that the epilogue warps go
+// on while they are stored (8192 x 4096 x 14336: 484 us, 472 so; 32768 rows of 64 experts: 146
+// and 141). Single CTAs would pay for it with the depth of their ring (16 tokens x 2 of 8 experts
+// of 14336 x 4096: 87 and 90), fp32 would not fit.
+template <bool PAIR, typename Y>
+constexpr bool kAsyncStore = PAIR && sizeof(Y) == 2;
+
 // A tile of BN weight rows, made by one CTA or a pair.
-template <bool PAIR, int BN>
+template <bool PAIR, int BN, bool ASYNC>
 struct Wide {
     static constexpr int kCtas = PAIR ? 2 : 1;
     static constexpr int kRows = 128 * kCtas;    // rows of x a tile
     static constexpr int kOwnCols = BN / kCtas;  // weight rows that a CTA loads
     static constexpr int kXBytes = 128 * kBK;
     static constexpr int kStage = kXBytes + kOwnCols * kBK;
-    static constexpr int kStages = 196608 / kStage;  // 6 of 32 KB, 4 of 48
+    // shared memory of an epilogue warp for y: 32 rows x BN / 2 columns of 2 bytes, or the turning
+    static constexpr int kOut = ASYNC ? 32 * BN : kTurnBytes;
+    static constexpr int kStages = (ASYNC ? 131072 : 196608) / kStage;  // 4 or 6 of 32 KB, 4 of 48
     static constexpr int kBufs = 512 / BN;       // all 512 columns of tensor memory
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
     static size_t smem(int E) {
-        return 1024 + (size_t)kStages * kStage + 8 * kTurnBytes + (2 * kStages + 2 * kBufs + 1) * 8 + 16 +
+        return 1024 + (size_t)kStages * kStage + 8 * kOut + (2 * kStages + 2 * kBufs + 1) * 8 + 16 +
                (size_t)(2 * E + 2) * 4;
     }
 };
@@ -489,15 +498,29 @@ Q4_DEVINL uint32_t two(float lo, float hi) {
     }
 }
 
+// A tile out of shared memory, and the waits for such stores of this thread: until what they read
+// may be written again, and until they are done. (The copies end by themselves; no flag is
+// waited for.)
+Q4_DEVINL void tma_store_2d(const void *tmap, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+Q4_DEVINL void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+Q4_DEVINL void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+Q4_DEVINL void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 template <bool PAIR, int BN, typename Y>
 __global__ void __launch_bounds__(kWideThreads, 1)
-fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw) {
-    using W = Wide<PAIR, BN>;
+fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
+         const __grid_constant__ CUtensorMap tmy) {
+    constexpr bool ASYNC = kAsyncStore<PAIR, Y>;
+    using W = Wide<PAIR, BN, ASYNC>;
     constexpr int HALF = BN / 2;  // columns an epilogue warp keeps
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *turn = ring + W::kStages * W::kStage;
-    uint64_t *full = reinterpret_cast<uint64_t *>(turn + 8 * kTurnBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(turn + 8 * W::kOut);
     uint64_t *empty = full + W::kStages;
     uint64_t *dfull = empty + W::kStages;
     uint64_t *dempty = dfull + W::kBufs;
@@ -666,7 +689,27 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                 else return two<Y>(value(c), value(c + 1));
             };
             constexpr int IN4 = 4 / (int)sizeof(Y);  // columns in 4 bytes
-            if (vec) {
+            uint8_t *mine = turn + (warp - 4) * W::kOut;
+            const int first_row = rl - lane;
+            if (ASYNC && a.bulk && first_row + 32 <= t.rows) {
+                if (lane == 0) bulk_wait_read();  // the last tile's rows have left
+                __syncwarp();
+                // 64 columns after 64, rows of 128 bytes in the 128-byte swizzle
+#pragma unroll
+                for (int c = 0; c < HALF; c += 8) {
+                    uint8_t *at = mine + (c / 64) * 4096 + lane * 128 + (((c / 8) & 7) ^ (lane & 7)) * 16;
+                    *reinterpret_cast<uint4 *>(at) =
+                        make_uint4(word(c), word(c + IN4), word(c + 2 * IN4), word(c + 3 * IN4));
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < HALF; c += 64)
+                        if (n0 + c < a.N) tma_store_2d(&tmy, mine + (c / 64) * 4096, (int)n0 + c, t.row0 + first_row);
+                    bulk_commit();
+                }
+            } else if (vec) {
                 Y *yr = y + (int64_t)(t.row0 + rl) * a.N + n0;
 #pragma unroll
                 for (int c = 0; c < HALF; c += PER) {
@@ -680,8 +723,11 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                 // of fp32, 16 of two rows) side by side, not in 32 rows (4099 x 7801 x 880 in fp16:
                 // 348 us so, 58 this way)
                 constexpr int CH = 64 / (int)sizeof(Y);
-                uint8_t *mine = turn + (warp - 4) * kTurnBytes;
-                const int col = lane % CH, up = lane / CH, first_row = rl - lane;
+                const int col = lane % CH, up = lane / CH;
+                if constexpr (ASYNC) {
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int c = 0; c < HALF; c += CH) {
 #pragma unroll
@@ -699,6 +745,7 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                 }
             }
         }
+        if (ASYNC && lane == 0) bulk_wait();  // y is written
     }
     if (timed_out && a.status) atomicOr(a.status, Q4_STATUS_TIMEOUT);
     __syncwarp();
@@ -723,6 +770,19 @@ bool encode_codes_map(CUtensorMap *tm, const uint8_t *codes, int64_t rows, int64
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y [rows][N] of 2-byte values, stored by 32 rows x 64 columns.
+bool encode_rows_map(CUtensorMap *tm, void *y, int64_t rows, int64_t N) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)N * 2};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
 // Row tiles of `rows` rows: at most (which experts have rows is known on the device only).
@@ -777,14 +837,17 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
 
 template <bool PAIR, int BN, typename Y>
 cudaError_t launch_wide(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
-    using W = Wide<PAIR, BN>;
+    using W = Wide<PAIR, BN, kAsyncStore<PAIR, Y>>;
     const int64_t tiles = row_tiles(a, W::kRows) * ((a.N + BN - 1) / BN);
     // What a smaller box leaves of the x tile in shared memory is any codes: rows of D that are
     // not stored
     a.box = (int)std::min<int64_t>(128, (a.R + 7) / 8 * 8);
-    CUtensorMap tmx, tmw;
+    CUtensorMap tmx, tmw, tmy;
     if (!encode_codes_map(&tmx, x, a.R, K, a.box) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, W::kOwnCols))
         return cudaErrorInvalidValue;
+    a.bulk = kAsyncStore<PAIR, Y> && a.N % 8 == 0 && (uintptr_t)a.y % 16 == 0;
+    if (!a.bulk) tmy = tmx;  // not used
+    else if (!encode_rows_map(&tmy, a.y, a.R, a.N)) return cudaErrorInvalidValue;
     auto kern = fp8_wide<PAIR, BN, Y>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = once_per_device(ready, [&]() -> cudaError_t {
@@ -798,7 +861,7 @@ cudaError_t launch_wide(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K
     });
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)(W::kCtas * std::min<int64_t>(tiles, sms / W::kCtas));
-    return launch_overlapped(kern, grid, kWideThreads, W::smem(a.E), st, (unsigned)W::kCtas, a, tmx, tmw);
+    return launch_overlapped(kern, grid, kWideThreads, W::smem(a.E), st, (unsigned)W::kCtas, a, tmx, tmw, tmy);
 }
 
 template <typename Y>
@@ -859,7 +922,7 @@ q4_status fp8_product(const uint8_t *x, const float *xs, int64_t R, const int32_
     if (!x || !xs || !w || !ws || !y) return Q4_ERR_ARG;
     if ((uintptr_t)x % 16 || (uintptr_t)w % 16) return Q4_ERR_UNSUPPORTED;
     Fp8Args a{xs, ws, offsets, y, status, N, (int32_t)R, (int32_t)E, (int32_t)((N + 127) / 128),
-              (int32_t)((K + 127) / 128), 1, 0, 0};
+              (int32_t)((K + 127) / 128), 1, 0, 0, 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int sms = device_sms();
     const cudaError_t e = yt == Q4_F32    ? launch_fp8<float>(a, x, w, K, sms, st)

@@ -527,3 +527,24 @@ def test_static_weights_after_these_kernels(q4):
             f()
             y = q4.qgemm(x, payload, scales, 8192, 8192, 4, 128, weights_static=True)
             assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("N,off", [(256, 0), (264, 0), (200, 0), (272, 8), (264, 3)])
+@pytest.mark.parametrize("M", [1024, 1100])
+def test_pairs_store_their_rows(q4, M, N, off):
+    # experts of hundreds of rows (pairs of CTAs): full and partial groups of 32 rows, rows of whole
+    # and of partial 16-byte units, y at an offset, and the rows around it as they were
+    import torch
+
+    K, E = 128, 2
+    counts = [M - 513, 513]
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    p, (x, xs, w, ws) = problem(M + N, M, N, K, E)
+    for t in ("bf16", "f16", "f32"):
+        buf = torch.full((M * N + 64,), 5.0, device="cuda", dtype=dt(t))
+        y = buf[off:off + M * N].view(M, N)
+        for _ in range(2):
+            q4.fp8_gemm_grouped(x, xs, w, ws, torch.from_numpy(offsets).cuda(), out=y)
+        y64, mag = grouped_ref(p, offsets)
+        check(y, y64, mag, 1, t)
+        assert bool((buf[:off] == 5).all()) and bool((buf[off + M * N:] == 5).all())
