@@ -395,7 +395,9 @@ typedef enum q4_dtype {
  *           magnitudes above 448 held at 448.
  *   x        [x_rows][K] of type xt, row-major, any alignment (16-byte aligned rows are
  *            read fastest); with Q4_FP8_PACK_SILU_MUL [x_rows][2K], gate then up, and the
- *            values are v = silu(gate) * up = gate * up / (1 + exp(-gate)) in fp32
+ *            values are v = silu(gate) * up = gate * up / (1 + exp(-gate)) in fp32,
+ *            relative error at most (10 + 1.2 |gate|) 2^-23 (values below 2^-126 may
+ *            become 0); their quotients v / scale may be two fp32 units off
  *   rows     optional (may be NULL) [R] int32: output row i takes row rows[i] of x (the
  *            tokens of q4_moe_sort); an entry outside 0 .. x_rows - 1 leaves output row i as
  *            it was. Without it R must be x_rows.

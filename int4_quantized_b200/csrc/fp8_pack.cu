@@ -157,15 +157,18 @@ Q4_DEVINL uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// The codes of N values given negated.
-template <int N>
+// The codes of N values given negated. EXACT: of the correctly rounded quotients; else of the
+// products with the reciprocal, within two units of them, for values that are no more exact
+// themselves (silu, 8192 x 14336: 100 us with the corrections, 96 without).
+template <int N, bool EXACT>
 Q4_DEVINL void codes_of(const float (&nv)[N], const BlockDiv &d, uint32_t (&c)[N / 4]) {
     float q[N];
     if (d.nr != 0.f) {
         const uint64_t s = pair(d.s, d.s), nr = pair(d.nr, d.nr);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const float2 f = halves(quotients(pair(nv[i], nv[i + 1]), s, nr));
+            const uint64_t v = pair(nv[i], nv[i + 1]);
+            const float2 f = halves(EXACT ? quotients(v, s, nr) : mul2(v, nr));
             q[i] = f.x, q[i + 1] = f.y;
         }
     } else {
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(256, 5) fp8_pack_rows(const RowsArgs a) {
         d.nr = __shfl_sync(0xffffffffu, own.nr, j, 8);
         if (!on[j]) continue;
         uint32_t c[4];
-        codes_of<16>(nv[j], d, c);
+        codes_of<16, !SILU>(nv[j], d, c);
         uint8_t *p = a.codes + (int64_t)row[j] * a.K + (blk[j] * 128 + 16 * sub);
         if constexpr (VEC) {
             if (left[j] > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(c[0], c[1], c[2], c[3]);
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) fp8_pack_tiles(const T *w, in
         float nv[PER];
         raw[i].template values<true>(nv);
         uint32_t c[PER / 4];
-        codes_of<PER>(nv, d, c);
+        codes_of<PER, true>(nv, d, c);
         uint8_t *p = dst + n * K + k0;
         uint4 out = make_uint4(c[0], c[1], 0, 0);
         if constexpr (PER == 16) out.z = c[2], out.w = c[3];
