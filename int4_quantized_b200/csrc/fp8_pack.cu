@@ -179,14 +179,13 @@ Q4_DEVINL void codes_of(const float (&nv)[N], const BlockDiv &d, uint32_t (&c)[N
     for (int i = 0; i < N / 4; ++i) c[i] = e4m3x4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
 }
 
-// silu(g) u = g u / (1 + 2^(-g log2 e)) for two values, in fp32 with the hardware's exponential
-// and reciprocal, negated where u is given negated; results below 2^-126 are taken as 0.
+// silu(g) u = g u / (1 + 2^(-g log2 e)) for two values of which neither gate is below kFarGate, in
+// fp32 with the hardware's exponential and reciprocal, negated where u is given negated.
 // Error: t = g log2 e is off by at most |t| 2^-23 in all (its rounding and the constant's), so
 // 2^-t by |g| 2^-23 relative, to which the exponential, the sum, the reciprocal and the two
 // products add at most 8 x 2^-23. Of 12 million fp32 values 11 codes differ from those of 64
 // bits, as with fp32 exp and division (12); correcting t and the reciprocal changed that by
-// nothing and cost 17 us of 118 at 8192 x 14336. For gates below about -88 the sum is infinite
-// and the value 0.
+// nothing and cost 17 us of 118 at 8192 x 14336.
 Q4_DEVINL uint64_t silu_mul2(uint64_t g, uint64_t u) {
     constexpr float L = 1.4426950408889634f;
     const float2 t = halves(mul2(g, pair(-L, -L)));
@@ -196,6 +195,26 @@ Q4_DEVINL uint64_t silu_mul2(uint64_t g, uint64_t u) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
     return mul2(mul2(g, pair(r.x, r.y)), u);
+}
+
+// Below this gate the sum above nears 2^126, from where on its reciprocal is flushed to 0 (and from
+// 2^128 on the sum is infinite), however large u makes the value.
+constexpr float kFarGate = -87.f;
+// silu(g) u for g < kFarGate. There 1 / (1 + e^-g) is e^g to 2^-125: two factors of e^(g/2), on
+// either side of u, stay inside fp32's range wherever the value does: for gates down to -182 (then
+// even the largest u gives less than 2^-126) e^(g/2) is at least 2^-132, a subnormal number of 18
+// bits, which the two factors' 2^-18 each leave within the bound at such gates, (10 + 1.2 |g|) 2^-23.
+Q4_DEVINL float silu_mul_far(float g, float u) {
+    constexpr float L = 1.4426950408889634f;
+    float h;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(h) : "f"(0.5f * (g * L)));
+    return g * h * u * h;
+}
+// the least of three, NaN aside
+Q4_DEVINL float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 struct RowsArgs {
@@ -253,6 +272,7 @@ __global__ void __launch_bounds__(256, 5) fp8_pack_rows(const RowsArgs a) {
     }
     float nv[U][16];
     uint32_t m[U];
+    bool far[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
         if constexpr (SILU) {
@@ -264,9 +284,29 @@ __global__ void __launch_bounds__(256, 5) fp8_pack_rows(const RowsArgs a) {
                 const float2 f = halves(silu_mul2(pair(g[i], g[i + 1]), pair(u[i], u[i + 1])));
                 nv[j][i] = f.x, nv[j][i + 1] = f.y;
             }
+            float least = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) least = min3(least, g[i], g[i + 1]);
+            far[j] = least < kFarGate;
         } else {
             x[j].template values<true>(nv[j]);
         }
+    }
+    if constexpr (SILU) {  // rare: those values again, read again (kept, they would cost the registers)
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (!far[j]) continue;
+            const int64_t s = a.rows ? a.rows[row[j]] : row[j];
+            const T *p = static_cast<const T *>(a.x) + s * a.ldx + (blk[j] * 128 + 16 * sub);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float g = i < left[j] ? (float)p[i] : 0.f;
+                if (g < kFarGate) nv[j][i] = silu_mul_far(g, -(float)p[i + a.K]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; i += 2) big = abs_max(big, nv[j][i], nv[j][i + 1]);
