@@ -132,17 +132,25 @@ class Fp8Experts:
         return cls(*fp8_pack_weights(gate_up), *fp8_pack_weights(down))
 
     @staticmethod
-    def sorted_rows(x: torch.Tensor, tokens: torch.Tensor, status: Optional[torch.Tensor] = None
-                    ) -> Tuple[torch.Tensor, torch.Tensor]:
-        """(codes, scales) of x[tokens]: fp8_pack(x, rows=tokens), by the shorter way."""
+    def sorted_rows(x: torch.Tensor, tokens: torch.Tensor, status: Optional[torch.Tensor] = None,
+                    pos: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """(codes, scales) of x[tokens]: fp8_pack(x, rows=tokens), by the shorter way.
+
+        The status word takes what the rows in `tokens` give, whichever way is taken; the way by
+        each row once needs `pos` (moe_sort's) for that, to leave the other rows of x out.
+        """
         T, D = x.shape
         R = tokens.shape[0]
         # Packing in sorted order rounds a token's row once for each of its experts. From 2^25 values
         # on it is sooner done to round each row once and gather codes and scales (4096 tokens x 8 of
         # 2048 bf16 values: 41 us, and 23 this way); below, one launch is sooner than three.
-        if R * D < 1 << 25 or R <= T:
+        if R * D < 1 << 25 or R <= T or (status is not None and pos is None):
             return fp8_pack(x, rows=tokens, status=status)
-        xq, xs = fp8_pack(x, status=status)
+        rows = None
+        if status is not None:  # tokens without a place (padding) report nothing
+            own = torch.arange(T, dtype=torch.int32, device=x.device)
+            rows = torch.where(pos.amax(1) >= 0, own, -1)
+        xq, xs = fp8_pack(x, rows=rows, status=status)
         return moe_gather(xq.view(torch.bfloat16), tokens).view(E4M3), moe_gather(xs, tokens)
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
@@ -150,7 +158,7 @@ class Fp8Experts:
         """x [T, D], ids and weights [T, k] -> [T, D] of x's type.
 
         A choice with an id outside 0 .. E - 1 adds nothing. status: one int32 that takes
-        Q4_STATUS_NONFINITE and Q4_STATUS_TIMEOUT.
+        Q4_STATUS_NONFINITE (of rows that an expert takes) and Q4_STATUS_TIMEOUT.
         """
         _cuda(x, "x")
         if x.dim() != 2 or x.shape[1] != self.D or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
@@ -159,7 +167,7 @@ class Fp8Experts:
             raise ValueError(f"x and ids must be on {self.gate_up.device}")
         tokens, pos, offsets = moe_sort(ids, self.E)
         live = offsets[self.E:]  # rows that have an expert
-        xq, xs = self.sorted_rows(x, tokens, status)
+        xq, xs = self.sorted_rows(x, tokens, status, pos)
         # gate and up become codes of 4 bits next: bf16 keeps enough of them, and unlike fp16 their range
         between = torch.bfloat16 if x.dtype == torch.float16 else x.dtype
         h = fp8_gemm_grouped(xq, xs, self.gate_up, self.gate_up_scales, offsets, out_dtype=between, status=status)
