@@ -41,6 +41,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once.cuh"
 #include "overlap.cuh"
 #include "tcgen05.cuh"
 
@@ -791,20 +792,6 @@ int64_t row_tiles(const Fp8Args &a, int rows) {
 }
 
 constexpr size_t kSmemMax = 227 * 1024;
-
-// Runs set() the first time on each device (a bit of `ready` each; every time beyond the 64th).
-// Two threads may both run it, with the same result.
-template <typename F>
-cudaError_t once_per_device(std::atomic<uint64_t> &ready, F set) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-    if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = set();
-    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
-    return e;
-}
 
 template <int NT, typename Y>
 cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once.cuh"
 #include "overlap.cuh"
 
 namespace q4 {
@@ -392,6 +393,9 @@ inline unsigned row_grid(int64_t rows, int64_t chunks) {
     return (unsigned)((rows * chunks + 7) / 8);
 }
 
+// Each warp's histogram, and the three arrays of the block (one with a place more).
+constexpr size_t sort_smem(int64_t warps, int64_t E) { return (size_t)(warps * E + 3 * E + 1) * 4; }
+
 template <typename T>
 cudaError_t sort_launch(const void *ids, int64_t R, int k, int E, int32_t *tokens, int32_t *pos, int32_t *offsets,
                         cudaStream_t st) {
@@ -400,12 +404,14 @@ cudaError_t sort_launch(const void *ids, int64_t R, int k, int E, int32_t *token
     // and no more warps than chunks: every warp's histogram costs its clearing and its sum
     const int64_t chunks = (R + 31) / 32;
     const int warps = chunks >= kSortWarps ? kSortWarps : chunks < 4 ? 4 : (int)chunks;
-    const size_t smem = ((size_t)warps * E + 3 * (size_t)E + 1) * 4;
+    const size_t smem = sort_smem(warps, E);
     auto kern = moe_sort_kernel<T>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [&]() {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sort_smem(kSortWarps, kMaxExperts));
+    });
+    if (e != cudaSuccess) return e;
     return launch_overlapped(kern, ctas, 32 * warps, smem, st, ctas, static_cast<const T *>(ids), R, k, E, tokens, pos,
                              offsets);
 }

@@ -1,0 +1,62 @@
+"""Calls of one entry point from two host threads, each on a stream of its own: what a call asks of
+its kernel (the shared memory of a launch among it) must not depend on the other thread's calls."""
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q4():
+    import int4_quantized_b200 as m
+
+    m.lib()
+    return m
+
+
+def together(calls, rounds):
+    """Makes each call (of one stream's raw handle) `rounds` times in a thread and on a stream of its own; all
+    must return 0."""
+    import torch
+
+    torch.cuda.synchronize()
+    codes, start = [set() for _ in calls], threading.Barrier(len(calls))
+    streams = [torch.cuda.Stream() for _ in calls]
+
+    def run(i):
+        raw = streams[i].cuda_stream
+        start.wait()
+        for _ in range(rounds):
+            codes[i].add(calls[i](raw))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}] * len(calls), codes
+
+
+@pytest.mark.parametrize("bits", [32, 64])
+def test_sorts_of_different_sizes(q4, bits):
+    # 32 warps' histograms: 143 KB for 1024 experts, 56 KB for 400; the C entry point itself, which
+    # Python calls without its lock, so that the threads are inside it together
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(bits)
+    dtype = torch.int32 if bits == 32 else torch.int64
+    T, k = 600, 2
+    cases, calls = [], []
+    for E in (1024, 400, 900, 500):
+        ids = torch.randint(-1, E, (T, k), device="cuda", generator=g).to(dtype)
+        want = q4.moe_sort(ids, E)
+        got = [torch.full_like(t, -9) for t in want]
+        args = (ids.data_ptr(), bits, T, k, E, *(t.data_ptr() for t in got))
+        cases.append((want, got, ids))
+        calls.append(lambda stream, args=args: q4.lib().q4_moe_sort(*args, stream))
+    together(calls, 20000)
+    for want, got, _ in cases:
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
