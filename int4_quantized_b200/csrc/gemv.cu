@@ -666,7 +666,8 @@ cudaError_t dispatch_gemv(const GemvPlan &pl, const GemvArgs &a, const CUtensorM
 
 }  // namespace
 
-EncodeTiledFn encode_fn() {
+// The driver's encoder, or null.
+EncodeTiledFn driver_encode() {
     static EncodeTiledFn fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -677,6 +678,23 @@ EncodeTiledFn encode_fn() {
     }();
     return fn;
 }
+
+// The encoder is a driver call and fails in a host thread without a current context, such as one
+// whose first CUDA call this is (a launch by the runtime would bind one): bind the current
+// device's then, and encode again.
+CUresult encode_tiled(CUtensorMap *tm, CUtensorMapDataType type, cuuint32_t rank, void *base, const cuuint64_t *dims,
+                      const cuuint64_t *strides, const cuuint32_t *box, const cuuint32_t *steps,
+                      CUtensorMapInterleave interleave, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2,
+                      CUtensorMapFloatOOBfill fill) {
+    const EncodeTiledFn enc = driver_encode();
+    CUresult r = enc(tm, type, rank, base, dims, strides, box, steps, interleave, swizzle, l2, fill);
+    int dev = 0;
+    if (r != CUDA_SUCCESS && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = enc(tm, type, rank, base, dims, strides, box, steps, interleave, swizzle, l2, fill);
+    return r;
+}
+
+EncodeTiledFn encode_fn() { return driver_encode() ? encode_tiled : nullptr; }
 
 bool encode_payload_map(CUtensorMap *tm, const uint8_t *payload, int64_t N, int64_t K, int bits, int box_rows) {
     EncodeTiledFn enc = encode_fn();

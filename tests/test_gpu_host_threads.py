@@ -60,3 +60,40 @@ def test_sorts_of_different_sizes(q4, bits):
     for want, got, _ in cases:
         for u, v in zip(got, want):
             assert torch.equal(u, v)
+
+
+def test_first_cuda_call_of_a_thread(q4):
+    # every entry point that a new thread may call before any other CUDA call of its own
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    N, K = 256, 1024
+    w = torch.randn(N, K, device="cuda", generator=g)
+    payload, scales = q4.qpack(w, 4, 128)
+    x, xb = torch.randn(1, K, device="cuda", generator=g), torch.randn(64, K, device="cuda", generator=g).bfloat16()
+    xq, wq = q4.fp8_pack(x), q4.fp8_pack_weights(w)
+    big, ids = q4.fp8_pack(xb), torch.randint(0, 4, (16, 2), device="cuda", generator=g)
+    offsets = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    calls = [lambda: q4.qgemm(x, payload, scales, N, K, 4, 128), lambda: q4.qgemm(xb, payload, scales, N, K, 4, 128),
+             lambda: q4.qpack(w, 8, 128)[0], lambda: q4.qdequant(payload, scales, (N, K), 4, 128),
+             lambda: q4.fp8_gemm(*xq, *wq), lambda: q4.fp8_gemm(*big, *wq),
+             lambda: q4.fp8_gemm_grouped(*big, wq[0][None], wq[1][None], offsets),
+             lambda: q4.fp8_pack(x)[1], lambda: q4.fp8_pack_weights(w)[1], lambda: q4.moe_sort(ids, 4)[1],
+             lambda: q4.moe_gather(xb, offsets[:1]), lambda: q4.moe_combine(xb, ids.int())]
+    want = [c() for c in calls]
+    got = [None] * len(calls)
+    torch.cuda.synchronize()
+
+    def run(i):
+        try:
+            got[i] = calls[i]()
+        except Exception as e:  # noqa: BLE001 (shown below, in the test's own thread)
+            got[i] = e
+
+    for i in range(len(calls)):
+        t = threading.Thread(target=run, args=(i,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert isinstance(a, torch.Tensor) and torch.equal(a, b), (i, a)
