@@ -47,6 +47,7 @@
 #include "common.cuh"
 #include "gemv_math.cuh"
 #include "kernels.h"
+#include "once.cuh"
 
 namespace q4 {
 
@@ -68,7 +69,8 @@ constexpr int kSG = 12;                            // scale slots per row per k-
 constexpr int kInkMaxK = 4096;                     // k of one CTA's range whose pieces are built on
                                                    // chip (32 KB at 8 bytes per k)
 constexpr int kSmemBudget2 = 115200;               // two CTAs per SM
-constexpr int kSmemBudget1 = 232448 - 1024;        // one CTA per SM (227 KB opt-in maximum)
+constexpr int kSmemMost = 232448;                  // 227 KB opt-in maximum
+constexpr int kSmemBudget1 = kSmemMost - 1024;     // one CTA per SM
 constexpr int kRedBytes = kRowsPerCta * 16 * 4;    // cluster partial sums, aliased on the ring
 
 struct GemvArgs {
@@ -589,7 +591,9 @@ cudaError_t launch_typed(const GemvPlan &pl, const GemvArgs &a, const CUtensorMa
     }
     auto kern = gemv_stream<BITS, L, NB, GPS, INK, XBF16, HYB, WIDE>;
     const size_t smem = pl.smem_bytes;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> ready{0};
+    err = once_per_device(
+        ready, [&]() { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost); });
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.clusters * pl.CS, pl.nmc);

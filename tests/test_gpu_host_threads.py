@@ -97,3 +97,26 @@ def test_first_cuda_call_of_a_thread(q4):
     torch.cuda.synchronize()
     for i, (a, b) in enumerate(zip(got, want)):
         assert isinstance(a, torch.Tensor) and torch.equal(a, b), (i, a)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_gemvs_of_different_lengths(q4, bits):
+    # one row of x: a CTA's share of K, and with it the shared memory of the launch, differs
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(bits)
+    N = 256
+    cases, calls = [], []
+    for K in (4096, 11008, 2048, 28672):
+        payload, scales = q4.qpack(torch.randn(N, K, device="cuda", generator=g), bits, 128)
+        x = torch.randn(1, K, device="cuda", generator=g)
+        want = q4.qgemm(x, payload, scales, N, K, bits, 128)
+        y = torch.zeros_like(want)
+        ws = torch.empty(max(256, q4.qgemm_workspace_bytes(1, N, K, bits, 128)), dtype=torch.uint8, device="cuda")
+        args = (x.data_ptr(), q4.Q4_X_F32, 1, payload.data_ptr(), scales.data_ptr(), N, K, bits, 128, y.data_ptr(), ws.data_ptr(),
+                ws.numel(), 0, None)
+        cases.append((want, y, x, payload, scales, ws))
+        calls.append(lambda stream, args=args: q4.lib().qgemm_ex(*args, stream))
+    together(calls, 20000)
+    for want, y, *_ in cases:
+        assert torch.equal(y, want)
