@@ -604,10 +604,13 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
                         filled = min(filled + 1, W::kStages);
                     }
                 }
-                // no copy may land after the pair has gone: the slots' last rounds
-                if (rank == 0)
-                    for (int i = 0; i < filled; ++i)
-                        timed_out |= !mbar_wait(full + i, i < s.i ? s.round : s.round ^ 1);
+                // no copy may land after the block has gone, and no arrival from the other block of a
+                // pair: the slots' last rounds, of a pair those in which the MMA has freed them (the
+                // copies lie before that; those of the second block are counted in the first alone)
+                bool ended = true;
+                for (int i = 0; i < filled && ended; ++i)
+                    ended = mbar_wait((PAIR ? empty : full) + i, i < s.i ? s.round : s.round ^ 1);
+                timed_out |= !ended;
             }
         } else if (warp == 1 && rank == 0) {
             // the whole warp keeps step and one lane issues: operands stay uniform across the warp
@@ -638,6 +641,8 @@ fp8_wide(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __grid_
             if (elect_one()) umma_commit_of<PAIR>(done);
             __syncwarp();
             timed_out |= !mbar_wait(done, 0);
+        } else if (warp == 1) {
+            timed_out = !mbar_wait(done, 0);  // the MMAs' last arrival in this block
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideHigh));

@@ -43,3 +43,13 @@ def test_every_wait_is_bounded():
     # nothing waits on a barrier but by mbar_wait
     s = text()
     assert not re.search(r"mbarrier\.(try_wait|test_wait)|mbar_try_wait|while \(true\)|for \(;;\)", s)
+
+
+def test_blocks_of_a_pair_wait_for_the_arrivals_they_get():
+    # the tensor core's arrivals go to the barriers of both blocks of a pair: each waits for its last
+    # ones before it may end (and its shared memory become another block's)
+    s = text()
+    wide = s[s.index("fp8_wide(const Fp8Args"):s.index("bool encode_codes_map")]
+    assert re.search(r"mbar_wait\(\(PAIR \? empty : full\) \+ i,", wide)
+    first, second = wide[wide.index("} else if (warp == 1 && rank == 0) {"):].split("} else if (warp == 1) {", 1)
+    assert "mbar_wait(done, 0)" in first and "mbar_wait(done, 0)" in second.split("}", 1)[0]
