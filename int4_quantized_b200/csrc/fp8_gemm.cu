@@ -45,6 +45,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "fp8_plan.h"
 #include "kernels.h"
 #include "once.cuh"
 #include "overlap.cuh"
@@ -190,7 +191,7 @@ template <int NT>
 struct Stream {
     static constexpr int kXBytes = NT * kBK;
     static constexpr int kStage = kWBytes + kXBytes;
-    static constexpr int kBufs = 8;                      // tensor-memory buffers of NT columns
+    static constexpr int kBufs = kStreamBufs;            // tensor-memory buffers of NT columns
     static constexpr int kCols = kBufs * NT;             // 128 to 512 columns
     // one warp an SM quarter adds up to 32 columns a block of k before the next block's sums
     // are there; wider tiles take two (with one, 128 columns took 0.9 us a block, the loads and
@@ -199,11 +200,6 @@ struct Stream {
     static constexpr int kOwn = NT * 4 / kEpiWarps;      // columns a warp keeps
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kWRows >> 4) << 24);
-    // ring, exchange buffer of the split sums, scales, barriers
-    static size_t smem(int stages, int split, int E) {
-        return 1024 + (size_t)stages * kStage + (split > 1 ? (size_t)kWRows * NT * 4 : 0) + kBufs * NT * 4 +
-               (2 * (size_t)stages + 3 * kBufs + 2) * 8 + 16 + (size_t)(2 * E + 2) * 4;
-    }
 };
 
 template <int NT, typename Y>
@@ -804,24 +800,13 @@ int64_t row_tiles(const Fp8Args &a, int rows) {
     return a.offsets ? std::min((int64_t)a.R, (int64_t)a.E + a.R / rows) : (a.R + rows - 1) / rows;
 }
 
-constexpr size_t kSmemMax = 227 * 1024;
-
 template <int NT, typename Y>
 cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t K, int sms, cudaStream_t st) {
     using S = Stream<NT>;
     const int64_t tiles = row_tiles(a, NT) * a.nb;
-    // K is split over a cluster while the CTAs still fit on the machine at once, every CTA
-    // keeps two blocks of k or more, and each takes whole columns of the joined sums
-    a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= sms && a.kb >= a.split * 4) a.split *= 2;
-    a.stages = (int)((kSmemMax - S::smem(0, a.split, a.E)) / (S::kStage + 16));
-    const int64_t blocks = (int64_t)((a.kb + a.split - 1) / a.split) * ((tiles + sms - 1) / sms);
-    a.stages = (int)std::max<int64_t>(2, std::min<int64_t>(std::min(a.stages, 16), blocks));
-    size_t smem = S::smem(a.stages, a.split, a.E);
-    // CTAs of a cluster wait for one another with their tensor memory held: two kernels that could
-    // not both have theirs on an SM must not meet there, or each could hold what the other's
-    // cluster waits for. Over half of the shared memory keeps them apart.
-    if (S::kCols > 128) smem = std::max(smem, kSmemMax / 2 + 1024);
+    const StreamPlan plan = stream_plan(NT, tiles, a.kb, a.E, sms);
+    a.split = plan.split;
+    a.stages = plan.stages;
     CUtensorMap tmx, tmw;
     if (!encode_codes_map(&tmx, x, a.R, K, NT) || !encode_codes_map(&tmw, w, (int64_t)a.E * a.N, K, kWRows))
         return cudaErrorInvalidValue;
@@ -832,7 +817,7 @@ cudaError_t launch_stream(Fp8Args a, const uint8_t *x, const uint8_t *w, int64_t
     });
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)(a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms));
-    return launch_overlapped(kern, grid, S::kThreads, smem, st, (unsigned)a.split, a, tmx, tmw);
+    return launch_overlapped(kern, grid, S::kThreads, plan.smem, st, (unsigned)a.split, a, tmx, tmw);
 }
 
 template <bool PAIR, int BN, typename Y>
