@@ -869,25 +869,11 @@ cudaError_t launch_fp8(const Fp8Args &a, const uint8_t *x, const uint8_t *w, int
             return launch_stream<64, Y>(a, x, w, K, sms, st);
         }
     }
-    // The shape of fp8_wide's tiles by the rounds they take: a round of 256 x 256 by pairs, of
-    // 128 x 256 and of 128 x 128 by single CTAs takes times as 19 : 20 : 15 (4096 x 4096, 512
-    // rows, one round of each: 20.1, 21.1 and 17.4 us; 11008 x 4096, 333 rows, 2, 1 and 2 rounds:
-    // 36.4, 21.2 and 29.7).
-    auto rounds = [&](int rows, int width, int64_t at_once) {
-        // row tiles: experts with less than half a tile of rows have one each, others on average
-        // half a tile more than their rows fill
-        const int64_t E = a.offsets ? a.E : 1, R = a.R;
-        const int64_t rt = !a.offsets ? (R + rows - 1) / rows : R * 2 < E * rows ? std::min(R, E) : R / rows + (E + 1) / 2;
-        return (rt * ((a.N + width - 1) / width) + at_once - 1) / at_once;
-    };
-    const int64_t pair = 19 * rounds(256, 256, sms / 2), single = 20 * rounds(128, 256, sms),
-                  narrow = 15 * rounds(128, 128, sms);
-    // (64 experts of 1408 x 2048 with 512 rows each: pairs 138 us, single CTAs 149, at 13 and 12
-    // rounds: many rounds together are slower by what they ask of L2)
-    if (a.offsets ? a.R >= 512 * (int64_t)a.E : pair <= single && pair <= narrow)
-        return launch_wide<true, 256, Y>(a, x, w, K, sms, st);
-    if (narrow < single) return launch_wide<false, 128, Y>(a, x, w, K, sms, st);
-    return launch_wide<false, 256, Y>(a, x, w, K, sms, st);
+    switch (wide_shape(a.offsets != nullptr, a.E, a.N, a.R, sms)) {
+        case kWidePair: return launch_wide<true, 256, Y>(a, x, w, K, sms, st);
+        case kWideNarrow: return launch_wide<false, 128, Y>(a, x, w, K, sms, st);
+        default: return launch_wide<false, 256, Y>(a, x, w, K, sms, st);
+    }
 }
 
 int device_sms() {

@@ -1,9 +1,9 @@
 """The tile shapes of fp8_gemm and the lane layouts of fp8_pack that large calls take.
 
-Which shapes of N and rows reach which tiles (128-row blocks of 148 SMs): a dense product of 333
-rows and N of 9473 to 12544 is one round of 128 x 256 tiles and two of the others; of 300 rows and
-N of 9217 to 9472 one round of 256 x 256 tiles by pairs of CTAs; few rows of four experts of 9472
-rows one round of 128 x 256. K from one block of 128 to more than any ring holds, and ragged.
+Which sizes reach which tiles is wide_shape's choice in csrc/fp8_plan.h (148 SMs): a dense product of
+333 rows and N of 9473 to 12544 is one round of 128 x 256 tiles and two of the others; pairs of CTAs
+make products of three rounds and more. K from one block of 128 to more than any ring holds, and
+ragged.
 
 Products are compared, all of y, with float64 products of the same codes on the GPU. Within a block
 of 128 the products are exact and each of at most 128 additions is off by at most 2^-23 of the
@@ -68,7 +68,8 @@ def check(y, ref, K, y_type):
 @pytest.mark.parametrize("y_type", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,K", [
     (333, 11008, 4096), (333, 10001, 1040), (300, 12000, 144), (257, 11008, 640), (300, 9473, 1040),  # 128 x 256
-    (300, 9472, 2064), (300, 9471, 1040), (1500, 9472, 656), (1411, 9328, 4096),  # pairs, one and several rounds
+    (300, 9472, 2064), (300, 9471, 1040),
+    (1500, 9472, 656), (1411, 9328, 4096), (1511, 9471, 400), (2045, 6152, 2064),  # pairs
     (512, 4096, 4096), (200, 4104, 1936), (700, 2305, 5008),                       # 128 x 128
 ])
 def test_gemm_tiles(q4, M, N, K, y_type):
@@ -90,8 +91,8 @@ def test_gemm_tiles(q4, M, N, K, y_type):
 @pytest.mark.parametrize("y_type", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("counts,N,K", [
     ([8, 0, 11, 13], 9472, 2064), ([1, 2, 30, 0], 9470, 272), ([4] * 8, 4736, 4096),  # few rows: 128 x 256
-    ([700, 0, 513, 1300], 1408, 1936), ([2048, 600], 2304, 656), ([900, 1100], 9001, 400),  # hundreds: pairs
-    ([130, 60, 0, 257, 1], 1408, 2064),
+    ([700, 0, 513, 1300], 1408, 1936), ([2048, 600], 2304, 656), ([130, 60, 0, 257, 1], 1408, 2064),
+    ([900, 1100], 9001, 400), ([2047, 2050], 2312, 2064), ([1500, 1500, 1200, 1], 2340, 1936),  # pairs
 ])
 def test_grouped_tiles(q4, counts, N, K, y_type):
     import torch
@@ -111,7 +112,31 @@ def test_grouped_tiles(q4, counts, N, K, y_type):
     assert bool((out[R:] == 3).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(333, 11008, 656), (300, 9472, 656)])
+@pytest.mark.parametrize("N,off", [(2304, 0), (2312, 0), (2312, 8), (2312, 3), (2305, 0), (2320, 5)])
+def test_pairs_write_their_rows_only(q4, N, off):
+    # full and partial groups of 32 rows, rows of whole and of partial 16-byte units, y at an offset, the
+    # rows of no expert and all around y as they were; twice, the second over the first's answers
+    import torch
+
+    counts, head, tail, K = [2047, 0, 2050], 2, 5, 144
+    at = np.concatenate([[head], head + np.cumsum(counts)])
+    R = int(at[-1]) + tail
+    gen = torch.Generator(device="cuda").manual_seed(N + off)
+    x, xs = codes(gen, 1, R, K)
+    w, ws = codes(gen, 128, 3, N, K)
+    for y_type in ("bf16", "f16", "f32"):
+        buf = torch.full((R * N + 64,), 5.0, device="cuda", dtype=dt(y_type))
+        y = buf[off:off + R * N].view(R, N)
+        for _ in range(2):
+            q4.fp8_gemm_grouped(x, xs, w, ws, torch.from_numpy(at.astype(np.int32)).cuda(), out=y)
+        for e, (a, b) in enumerate(zip(at, at[1:])):
+            if b > a:
+                check(y[a:b], product(x[a:b], xs[a:b], w[e], ws[e]), K, y_type)
+        assert bool((y[:head] == 5).all()) and bool((y[R - tail:] == 5).all())
+        assert bool((buf[:off] == 5).all()) and bool((buf[off + R * N:] == 5).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(333, 11008, 656), (300, 9472, 656), (1500, 9472, 656)])
 def test_large_tiles_keep_bad_rows_apart(q4, M, N, K):
     import torch
 
