@@ -228,10 +228,14 @@ struct RowsArgs {
     uint32_t units, kb;  // blocks in all, blocks a row
 };
 
-// Five CTAs an SM (51 registers a thread, some of them spilled once): left to itself the compiler
-// takes what leaves three or four, and 8192 x 14336 with silu takes 130 us instead of 101.
+// CTAs an SM. Left to itself the compiler takes the registers of three, and bf16 at 8192 x 14336 with
+// silu takes 102 us where five (48 registers, two-block groups spill 30 to 70 bytes) take 94, rows 76
+// and 67; fp32 rows 103 and 96. fp32 with silu, whose loads alone are 64 registers in two blocks,
+// spills 260 to 580 bytes at five: 282 us, with three (80 registers, 28 bytes at the most) 152.
+template <typename T, bool SILU, int U>
+constexpr int kRowsCtas = SILU && sizeof(T) == 4 && U == 2 ? 3 : 5;
 template <typename T, bool SILU, bool VEC, int U>
-__global__ void __launch_bounds__(256, 5) fp8_pack_rows(const RowsArgs a) {
+__global__ void __launch_bounds__(256, (kRowsCtas<T, SILU, U>)) fp8_pack_rows(const RowsArgs a) {
     begin_overlapped();
     const int sub = threadIdx.x & 7;
     const uint32_t first = blockIdx.x * (32 * U) + (threadIdx.x >> 3);
