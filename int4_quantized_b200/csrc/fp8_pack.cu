@@ -217,6 +217,21 @@ Q4_DEVINL float min3(float a, float b, float c) {
     return r;
 }
 
+// One value, of rows of any alignment byte by byte.
+template <typename T, bool VEC>
+Q4_DEVINL float load_one(const T *p) {
+    if constexpr (VEC) {
+        return (float)*p;
+    } else {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) v |= (uint32_t)reinterpret_cast<const uint8_t *>(p)[i] << (8 * i);
+        float f[16 / sizeof(T)];
+        unpack16<T, false>(make_uint4(v, 0, 0, 0), f);
+        return f[0];
+    }
+}
+
 struct RowsArgs {
     const void *x;
     const int32_t *rows;   // source row of each output row, or null
@@ -304,8 +319,8 @@ __global__ void __launch_bounds__(256, (kRowsCtas<T, SILU, U>)) fp8_pack_rows(co
             const T *p = static_cast<const T *>(a.x) + s * a.ldx + (blk[j] * 128 + 16 * sub);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float g = i < left[j] ? (float)p[i] : 0.f;
-                if (g < kFarGate) nv[j][i] = silu_mul_far(g, -(float)p[i + a.K]);
+                const float g = i < left[j] ? load_one<T, VEC>(p + i) : 0.f;
+                if (g < kFarGate) nv[j][i] = silu_mul_far(g, -load_one<T, VEC>(p + i + a.K));
             }
         }
     }

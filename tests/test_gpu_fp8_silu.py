@@ -117,3 +117,30 @@ def test_gates_too_far_for_any_up_give_zero(q4):
     x[0, :128] = torch.linspace(-3e38, -200, 128)
     codes, scales = q4.fp8_pack(x, silu_mul=True)
     assert bool((codes.float() == 0).all()) and bool((scales == 1).all())
+
+
+@pytest.mark.parametrize("x_type", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("M,K", [(9, 200), (9, 256), (2400, 1024)])
+@pytest.mark.parametrize("at", [1, 3, 6])
+def test_rows_at_any_byte(q4, x_type, silu, M, K, at):
+    # "any alignment": rows that do not begin at a whole element, through the C entry point
+    import torch
+
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[x_type]
+    cases = [c for c in FAR if x_type != "f16" or c in ((-86.5, 1.0), (-87.5, 1e4))] + [(0.0, 1.0), (3.0, 1.0)]
+    rows = far_rows(np.random.default_rng(at), M, K, cases)
+    x = torch.from_numpy(rows if silu else rows[:, K:].copy()).to(dtype).cuda()
+    want = q4.fp8_pack(x, silu_mul=silu)
+    n = x.numel() * x.element_size()
+    raw = torch.zeros(n + 16, dtype=torch.uint8, device="cuda")
+    raw[at:at + n] = x.view(torch.uint8).view(-1)
+    codes = torch.zeros(M * K + 16, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros_like(want[1])
+    torch.cuda.synchronize()
+    code = q4.lib().q4_fp8_pack(raw.data_ptr() + at, {"f32": 0, "bf16": 1, "f16": 2}[x_type], M, K, None, M, None, int(silu),
+                                codes.data_ptr() + at, scales.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    assert torch.equal(scales, want[1])
+    assert torch.equal(codes[at:at + M * K].view(M, K), want[0].view(torch.uint8))
+    assert int(codes[:at].sum()) == 0 and int(codes[at + M * K:].sum()) == 0
