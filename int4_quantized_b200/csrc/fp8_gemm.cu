@@ -315,12 +315,12 @@ fp8_stream(const Fp8Args a, const __grid_constant__ CUtensorMap tmx, const __gri
         if (elect_one()) umma_commit(done);
         __syncwarp();
         timed_out |= !mbar_wait(done, 0);
-    } else if (warp == 2) {
+    } else if (warp == 2) {  // each lane copies and arrives by itself, and may leave so
         Slot d;
         for (int64_t j = tile0; j < tiles && !timed_out; j += step) {
             const Tile t = tile_at(a, NT, a.nb, first, rows0, j);
             for (int kb = k0; kb < k1; ++kb) {
-                timed_out = __any_sync(0xffffffffu, !mbar_wait(dempty + d.i, d.round ^ 1));
+                timed_out = !mbar_wait(dempty + d.i, d.round ^ 1);
                 if (timed_out) break;
 #pragma unroll
                 for (int c = 0; c < NT; c += 32) {

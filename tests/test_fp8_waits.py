@@ -3,7 +3,8 @@
 A wait is bounded by a timer that each lane reads by itself, so where one runs out the lanes of a warp
 may disagree. Running out cannot be provoked without a fault in the kernel, so the rule that keeps
 the end of such a kernel defined is checked in the text: a lane leaves a loop on its own finding
-only where it works alone (under `if (lane == 0)`), else the warp votes first.
+only where it works alone (under `if (lane == 0)`), or where nothing in the loop is the whole warp's
+(warp 2, whose lanes copy scales); else the warp votes first.
 """
 import os
 import re
@@ -33,7 +34,12 @@ def test_a_warp_leaves_a_loop_together():
     jumps = [m.start() for m in re.finditer(r"if \(timed_out\) break;|timed_out = true;\s*break;", s)]
     assert len(jumps) >= 6
     for at in jumps:
-        if any(re.fullmatch(r"if \(lane == 0\)", h) for h in opened_before(s, at)):
+        heads = opened_before(s, at)
+        if any(re.fullmatch(r"if \(lane == 0\)", h) for h in heads):
+            continue
+        if any(re.fullmatch(r"(else )?if \(warp == 2\)", h) for h in heads):
+            body = s[s.rfind("warp == 2", 0, at):s.index("cp.async.wait_all", at)]
+            assert not re.search(r"_sync\(|__sync|elect_one|tmem_|cluster_|\.aligned|named_barrier", body)
             continue
         decided = s[s.rfind("mbar_wait(", 0, at) - 80:at]
         assert re.search(r"__(any|all)_sync\(0xffffffffu", decided), f"line {s.count(chr(10), 0, at) + 1}: lanes leave by themselves"
