@@ -436,8 +436,10 @@ Q4_API q4_status q4_fp8_pack_weights(const void *w, q4_dtype wt, int64_t E, int6
  *   status_word  as qgemm's: Q4_STATUS_TIMEOUT where a bounded wait gave up
  * K must be a multiple of 16 (else Q4_ERR_UNSUPPORTED), M and N are any. No workspace. The
  * inner sums are exact products added in fp32 on the tensor cores; the order of all sums
- * depends on the sizes only, so results are the same on every run. A row of x that holds NaN
- * codes affects its own row of y alone.
+ * depends on the sizes only, so results are the same on every run. The product of the two scales
+ * is rounded to fp32 by itself: where it leaves fp32's normal range (2^-126 to 2^128) y loses bits,
+ * becomes 0 or is not finite, also where the sum alone would bring it back. A row of x that holds
+ * NaN codes affects its own row of y alone.
  * Errors: Q4_ERR_ARG (null pointers, types, sizes), Q4_ERR_UNSUPPORTED (K % 16, M, N or K >
  * 2^30, misaligned codes), Q4_ERR_CUDA. M == 0 or N == 0 enqueues nothing.
  */

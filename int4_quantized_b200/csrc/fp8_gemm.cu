@@ -19,8 +19,8 @@
 // Many rows (fp8_wide): one CTA makes a tile of 128 rows of x x 256 or 128 weight rows, or a
 // pair of CTAs (cta_group::2) one of 256 x 256. In a pair each CTA loads its own rows of x and
 // half of the weights, so that a block of k costs an SM 32 KB from L2 instead of 48 (which
-// single CTAs take at 60 bytes a clock, about all that an SM can); the smaller tiles leave
-// fewer rows empty and fill the machine sooner. Here D's lanes are rows of x, so that the
+// single CTAs take at 60 bytes a clock); the smaller tiles leave fewer rows empty and fill the
+// machine sooner. Here D's lanes are rows of x, so that the
 // scale of a thread's whole row of D is one number a block of k. A block's time is the
 // epilogue's: with two buffers of all columns, an MMA, its epilogue and the signals between
 // them share the time of two blocks (8192 x 4096 x 14336, as first built: no epilogue work 378

@@ -183,9 +183,9 @@ Q4_DEVINL void codes_of(const float (&nv)[N], const BlockDiv &d, uint32_t (&c)[N
 // fp32 with the hardware's exponential and reciprocal, negated where u is given negated.
 // Error: t = g log2 e is off by at most |t| 2^-23 in all (its rounding and the constant's), so
 // 2^-t by |g| 2^-23 relative, to which the exponential, the sum, the reciprocal and the two
-// products add at most 8 x 2^-23. Of 12 million fp32 values 11 codes differ from those of 64
-// bits, as with fp32 exp and division (12); correcting t and the reciprocal changed that by
-// nothing and cost 17 us of 118 at 8192 x 14336.
+// products add at most 8 x 2^-23. Of 12 million fp32 values 12 and 11 codes (two seeds) differ from
+// those of 64 bits, as with fp32 exp and division (12 and 10); of fp16 values 9 and 9 (8 and 14).
+// Correcting t and the reciprocal changed that by nothing and cost 17 us of 118 at 8192 x 14336.
 Q4_DEVINL uint64_t silu_mul2(uint64_t g, uint64_t u) {
     constexpr float L = 1.4426950408889634f;
     const float2 t = halves(mul2(g, pair(-L, -L)));

@@ -7,7 +7,7 @@
 
 Codes are torch.float8_e4m3fn tensors. This module only marshals arguments for libq4's entry
 points q4_fp8_pack, q4_fp8_pack_weights, q4_fp8_gemm and q4_fp8_gemm_grouped (include/q4.h
-has the definitions); there is no CPU fallback.
+has the definitions); there is no CPU fallback. None of them registers with autograd.
 """
 from __future__ import annotations
 
