@@ -148,7 +148,8 @@ class Fp8Experts:
         # to 10, 2^24 11.3 and 9.2 to 12.9, 2^25 21 and 13 (8 experts a token, rows of 2048 and 4096),
         # 15 (4, of 7168), 18 (8, of 512), 21 to 22 (2); 2^27 77 and 37 to 56, with 2 a token 80 and 76
         # to 85. In fp32 the same, but for 2 a token 26 and 28 to 29 at 2^25, 111 and 94 to 103 at 2^27.
-        if R * D < 1 << 25 or R <= T or (status is not None and pos is None):
+        # (codes are gathered two by two, as 16-bit values)
+        if R * D < 1 << 25 or R <= T or D % 2 or (status is not None and pos is None):
             return fp8_pack(x, rows=tokens, status=status)
         rows = None
         if status is not None:  # tokens without a place (padding) report nothing
